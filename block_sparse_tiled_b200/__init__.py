@@ -13,6 +13,12 @@ The functions mirror the C ABI in ``include/vsa.h``:
     vsa_topk_select     S4  top-k key tiles per video query tile + compression
     vsa_sparse_attn_fwd S5  block-sparse attention + gated epilogue
     vsa_forward             S2..S5 in one call
+
+and the operators of a transformer block on either side of it:
+
+    vsa_rms_norm        RMS norm with the residual's addition, bf16 or 8-bit output
+    vsa_qk_rope         head norm and multi-axis rotary positions of Q and K
+    vsa_packed_attn     attention over packed whole prompts (vsa_packed_plan)
 """
 from __future__ import annotations
 
@@ -37,6 +43,9 @@ EXPORTED = (
     "vsa_gather_tiles", "vsa_pool_and_score", "vsa_topk_select", "vsa_sparse_attn_fwd", "vsa_forward",
     "vsa_forward_noalloc", "vsa_forward_host", "vsa_forward_host_workspace", "vsa_forward_parts", "vsa_wait_selftest",
     "vsa_plan_workspace", "vsa_device_status", "vsa_last_error", "vsa_version",
+    "vsa_rms_norm", "vsa_rope_create", "vsa_rope_table", "vsa_rope_destroy", "vsa_qk_rope",
+    "vsa_packed_plan", "vsa_packed_query", "vsa_packed_info", "vsa_packed_destroy", "vsa_packed_attn",
+    "vsa_packed_status",
 )
 
 
@@ -88,6 +97,63 @@ class WorkspaceLayout(ctypes.Structure):
                           "q_c", "k_c", "q_n8", "kv_max8", "k_sum", "k_mu", "total")]
 
 
+class RmsNormArgs(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("width", ctypes.c_int32), ("residual_f32", ctypes.c_int32),
+        ("weight_f32", ctypes.c_int32), ("out_e4m3", ctypes.c_int32), ("eps", ctypes.c_float),
+        ("x", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+        ("out", ctypes.c_void_p), ("residual_out", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+        ("x_stride", ctypes.c_int64), ("residual_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64),
+        ("residual_out_stride", ctypes.c_int64),
+    ]
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [
+        ("head_dim", ctypes.c_int32), ("n_axes", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+        ("shared_ladder", ctypes.c_int32), ("sections", ctypes.POINTER(ctypes.c_int32)), ("theta", ctypes.c_double),
+        ("inv_freq", ctypes.POINTER(ctypes.c_double)), ("axis", ctypes.POINTER(ctypes.c_int32)),
+    ]
+
+
+class QkRopeArgs(ctypes.Structure):
+    _fields_ = [
+        ("tokens", ctypes.c_int64), ("pos_rows", ctypes.c_int64), ("heads", ctypes.c_int32),
+        ("kv_heads", ctypes.c_int32), ("positions_f32", ctypes.c_int32), ("eps", ctypes.c_float),
+        ("positions", ctypes.c_void_p), ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("q_out", ctypes.c_void_p),
+        ("k_out", ctypes.c_void_p), ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+        *[(n, ctypes.c_int64) for n in ("q_stride", "q_head_stride", "k_stride", "k_head_stride", "q_out_stride",
+                                        "q_out_head_stride", "k_out_stride", "k_out_head_stride")],
+    ]
+
+
+class PackedDesc(ctypes.Structure):
+    _fields_ = [
+        ("n_seqs", ctypes.c_int32), ("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32), ("causal", ctypes.c_int32), ("softmax_scale", ctypes.c_float),
+        ("lengths", ctypes.POINTER(ctypes.c_int32)),
+    ]
+
+
+class PackedDims(ctypes.Structure):
+    _fields_ = [
+        ("tokens", ctypes.c_int64), ("pairs", ctypes.c_int64), ("items", ctypes.c_int64), ("ctas", ctypes.c_int32),
+        ("tile_tokens", ctypes.c_int32), ("softmax_scale", ctypes.c_float),
+    ]
+
+    def as_dict(self):
+        return {f: getattr(self, f) for f, _ in self._fields_}
+
+
+class PackedArgs(ctypes.Structure):
+    _fields_ = [
+        ("tokens", ctypes.c_int64), ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        *[(n, ctypes.c_int64) for n in ("q_stride", "q_head_stride", "k_stride", "k_head_stride", "v_stride",
+                                        "v_head_stride", "out_stride", "out_head_stride")],
+    ]
+
+
 _lib = None
 
 
@@ -120,6 +186,17 @@ def load_library(path: str = LIB_PATH):
     lib.vsa_forward_parts.argtypes = [P, ctypes.POINTER(SeqParts), P, ctypes.c_size_t, P]
     lib.vsa_wait_selftest.argtypes = [P, ctypes.c_int64, P, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int32)]
     lib.vsa_device_status.argtypes = [P, P, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int32)]
+    lib.vsa_rms_norm.argtypes = [ctypes.POINTER(RmsNormArgs), P]
+    lib.vsa_rope_create.argtypes = [ctypes.POINTER(RopeDesc), ctypes.POINTER(P)]
+    lib.vsa_rope_table.argtypes = [P, P, P]
+    lib.vsa_rope_destroy.argtypes = [P]
+    lib.vsa_qk_rope.argtypes = [P, ctypes.POINTER(QkRopeArgs), P]
+    lib.vsa_packed_plan.argtypes = [ctypes.POINTER(PackedDesc), P, ctypes.POINTER(P)]
+    lib.vsa_packed_query.argtypes = [ctypes.POINTER(PackedDesc), ctypes.c_int32, ctypes.POINTER(PackedDims), P, P]
+    lib.vsa_packed_info.argtypes = [P, ctypes.POINTER(PackedDims)]
+    lib.vsa_packed_destroy.argtypes = [P]
+    lib.vsa_packed_attn.argtypes = [P, ctypes.POINTER(PackedArgs), P]
+    lib.vsa_packed_status.argtypes = [P, P, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int32)]
     for name in EXPORTED:
         if name not in ("vsa_last_error", "vsa_version"):
             getattr(lib, name).restype = st
@@ -519,3 +596,336 @@ def workspace_views(plan, workspace):
         "idx": view(lay["idx"], B * H * V * (k + d["ref_topk"]), torch.int32, (B, H, V, k + d["ref_topk"])),
         "o_c": view(lay["o_c"], B * H * n_t * D, torch.float32, (B, H, n_t, D)),
     }
+
+
+# ---------------------------------------------------------------------------
+# Row operators around the attention
+# ---------------------------------------------------------------------------
+
+
+def _on_device(device, **tensors):
+    """Every given tensor is a CUDA tensor of `device`, and that is the current device (the library launches
+    on the current device, in its current stream unless one is given)."""
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.device != device or device.type != "cuda":
+            raise ValueError(f"{name} is on {t.device}: every tensor must be on one CUDA device")
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _rows(t, width, name):
+    """(rows, elements between rows) of a tensor whose last dimension is `width`: two-dimensional with unit
+    stride inside its rows, or contiguous."""
+    if t.dim() < 1 or t.shape[-1] != width:
+        raise ValueError(f"{name} must end in a dimension of {width}, got shape {tuple(t.shape)}")
+    if t.dim() == 2 and t.stride(1) == 1:
+        return t.shape[0], (t.stride(0) if t.shape[0] > 1 else width)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, or two-dimensional with contiguous rows")
+    return t.numel() // width, width
+
+
+def vsa_rms_norm(x, weight=None, eps=1e-6, residual=None, out=None, residual_out=None, scale=None, out_dtype=None,
+                 stream=None):
+    """Root-mean-square norm over the last dimension of x + residual, times weight, in one pass.
+
+    x: [..., C] bf16 (contiguous, or [rows, C] with any row stride that is a multiple of 8), C a multiple of 8
+    up to 16384; weight: [C] bf16 or float32, None for ones; residual: like x, bf16 or float32.
+    out_dtype (or the type of `out`): torch.bfloat16, or torch.float8_e4m3fn for 8-bit codes with one
+    float32 scale per row, scale = max|y| / 448 (out.float() * scale[..., None] is y, rounded).
+    residual_out receives x + residual in the residual's type (allocated when there is a residual; the residual
+    itself may be passed, and out may be x).  Returns (out, scale or None, residual_out or None)."""
+    _on_device(x.device, x=x, weight=weight, residual=residual, out=out, residual_out=residual_out, scale=scale)
+    if x.dtype != torch.bfloat16:
+        raise TypeError(f"x must be torch.bfloat16, got {x.dtype}")
+    if x.dim() < 1:
+        raise ValueError("x must have at least one dimension")
+    C = x.shape[-1]
+    if out is None:
+        out = torch.empty(x.shape, dtype=out_dtype or torch.bfloat16, device=x.device)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"out is {out.dtype}, out_dtype is {out_dtype}")
+    if out.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+        raise TypeError(f"the output type must be torch.bfloat16 or torch.float8_e4m3fn, got {out.dtype}")
+    f8 = out.dtype == torch.float8_e4m3fn
+    if C == 0:
+        raise ValueError("the last dimension of x is empty")
+    rows, x_ld = _rows(x, C, "x")
+    a = RmsNormArgs(rows=rows, width=C, out_e4m3=f8, eps=eps, x=x.data_ptr(), out=out.data_ptr(), x_stride=x_ld)
+    if out.shape != x.shape:
+        raise ValueError(f"out must have x's shape {tuple(x.shape)}, got {tuple(out.shape)}")
+    a.out_stride = _rows(out, C, "out")[1]
+    if weight is not None:
+        if weight.dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError(f"weight must be torch.bfloat16 or torch.float32, got {weight.dtype}")
+        if weight.shape != (C,) or not weight.is_contiguous():
+            raise ValueError(f"weight must be a contiguous [{C}], got {tuple(weight.shape)}")
+        a.weight, a.weight_f32 = weight.data_ptr(), weight.dtype == torch.float32
+    if f8:
+        if scale is None:
+            scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        if scale.dtype != torch.float32:
+            raise TypeError(f"scale must be torch.float32, got {scale.dtype}")
+        if scale.numel() != rows or not scale.is_contiguous():
+            raise ValueError(f"scale must be contiguous with one value for each of the {rows} rows")
+        a.scale = scale.data_ptr()
+    elif scale is not None:
+        raise ValueError("scale belongs to an 8-bit output")
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out needs a residual")
+    else:
+        if residual.dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError(f"residual must be torch.bfloat16 or torch.float32, got {residual.dtype}")
+        if residual.shape != x.shape:
+            raise ValueError(f"residual must have x's shape {tuple(x.shape)}, got {tuple(residual.shape)}")
+        if residual_out is None:
+            residual_out = torch.empty(x.shape, dtype=residual.dtype, device=x.device)
+        if residual_out.dtype != residual.dtype:
+            raise TypeError(f"residual_out must be {residual.dtype}, got {residual_out.dtype}")
+        if residual_out.shape != x.shape:
+            raise ValueError(f"residual_out must have x's shape {tuple(x.shape)}, got {tuple(residual_out.shape)}")
+        a.residual, a.residual_f32 = residual.data_ptr(), residual.dtype == torch.float32
+        a.residual_out = residual_out.data_ptr()
+        a.residual_stride = _rows(residual, C, "residual")[1]
+        a.residual_out_stride = _rows(residual_out, C, "residual_out")[1]
+    _check(load_library().vsa_rms_norm(ctypes.byref(a), _stream(stream)), "vsa_rms_norm")
+    return out, scale, residual_out
+
+
+class Rope:
+    """Owns a ``vsa_rope`` handle: the frequency and axis of every pair of a head row (host only)."""
+
+    def __init__(self, handle, head_dim, n_axes, interleaved):
+        self._h, self.head_dim, self.n_axes, self.interleaved = handle, head_dim, n_axes, interleaved
+
+    @property
+    def handle(self):
+        if self._h is None:
+            raise ValueError("rope destroyed")
+        return self._h
+
+    def table(self):
+        """(inv_freq float64 [head_dim / 2], axis int32 [head_dim / 2])."""
+        import numpy as np
+
+        freq, axis = np.empty(self.head_dim // 2), np.empty(self.head_dim // 2, np.int32)
+        _check(load_library().vsa_rope_table(self.handle, freq.ctypes.data, axis.ctypes.data), "vsa_rope_table")
+        return freq, axis
+
+    def destroy(self):
+        if self._h is not None:
+            load_library().vsa_rope_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.destroy()
+        except Exception:
+            pass
+
+
+def vsa_rope_create(head_dim, sections=None, theta=10000.0, interleaved=False, shared_ladder=False, inv_freq=None,
+                    axis=None, n_axes=None) -> Rope:
+    """Rotary positions of a head row of head_dim (64, 96 or 128): sections = rotated pairs per axis, e.g.
+    (16, 24, 24) for (time, height, width); pairs behind them do not turn.  The i-th of an axis's n pairs turns
+    theta^(-i / n) radians per step, with shared_ladder pair p of the head theta^(-p / (head_dim / 2)).  Or
+    inv_freq and axis, head_dim / 2 values each, give any other table (n_axes: 1 + the largest axis).
+    interleaved: pair p is elements (2p, 2p + 1), else (p, p + head_dim / 2)."""
+    d = RopeDesc(head_dim=int(head_dim), interleaved=int(bool(interleaved)), shared_ladder=int(bool(shared_ladder)),
+                 theta=float(theta))
+    if (inv_freq is None) != (axis is None):
+        raise ValueError("inv_freq and axis go together")
+    if inv_freq is not None:
+        if sections is not None:
+            raise ValueError("give sections, or inv_freq and axis")
+        freq, ax = [float(f) for f in inv_freq], [int(x) for x in axis]
+        if len(freq) != d.head_dim // 2 or len(ax) != d.head_dim // 2:
+            raise ValueError(f"inv_freq and axis need head_dim / 2 = {d.head_dim // 2} values each")
+        d.n_axes = int(n_axes) if n_axes is not None else 1 + max(ax)
+        keep = [(ctypes.c_double * len(freq))(*freq), (ctypes.c_int32 * len(ax))(*ax)]
+        d.inv_freq = ctypes.cast(keep[0], ctypes.POINTER(ctypes.c_double))
+        d.axis = ctypes.cast(keep[1], ctypes.POINTER(ctypes.c_int32))
+    else:
+        if sections is None:
+            raise ValueError("give sections, or inv_freq and axis")
+        sec = [int(s) for s in sections]
+        if n_axes is not None and n_axes != len(sec):
+            raise ValueError("n_axes must be the number of sections")
+        d.n_axes = len(sec)
+        keep = [(ctypes.c_int32 * max(1, len(sec)))(*sec)]
+        d.sections = ctypes.cast(keep[0], ctypes.POINTER(ctypes.c_int32))
+    h = ctypes.c_void_p()
+    _check(load_library().vsa_rope_create(ctypes.byref(d), ctypes.byref(h)), "vsa_rope_create")
+    return Rope(h, d.head_dim, d.n_axes, bool(interleaved))
+
+
+def _head_rows(t, D, name):
+    """(tokens, heads, elements between tokens, between heads) of [T, H, D], or of [B, L, H, D] whose tokens are
+    evenly spaced."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.dim() not in (3, 4) or t.shape[-1] != D:
+        raise ValueError(f"{name} must be [T, H, {D}] or [B, L, H, {D}], got {tuple(t.shape)}")
+    sh, st = t.shape, t.stride()
+    if st[-1] != 1:
+        raise ValueError(f"{name} must have contiguous head rows")
+    tokens, ld = sh[-3], st[-3]
+    if t.dim() == 4:
+        if sh[0] > 1 and sh[1] > 1 and st[0] != sh[1] * st[1]:
+            raise ValueError(f"{name}: the tokens of [B, L, H, D] must be evenly spaced")
+        tokens, ld = sh[0] * sh[1], (st[1] if sh[1] > 1 else st[0])
+    H = sh[-2]
+    hd = st[-2] if H > 1 else D
+    return tokens, H, (ld if tokens > 1 else H * D), hd
+
+
+def vsa_qk_rope(rope, q, k, positions, q_weight=None, k_weight=None, eps=1e-6, q_out=None, k_out=None, stream=None):
+    """Head norm (with q_weight / k_weight [D]) and rotary positions of q [T, H, D] and k [T, Hk, D] (or
+    [B, L, H, D]; any token and head strides that are multiples of 8, e.g. slices of one projection; k may be
+    None), bf16.  positions: [T, n_axes] int32 or float32, or [L, n_axes] for a batch of B sequences.  In place
+    with q_out = q, k_out = k.  Returns (q_out, k_out)."""
+    D = rope.head_dim
+    tokens, H, q_ld, q_hd = _head_rows(q, D, "q")
+    _on_device(q.device, q=q, k=k, positions=positions, q_weight=q_weight, k_weight=k_weight, q_out=q_out, k_out=k_out)
+    if positions.dtype not in (torch.int32, torch.float32):
+        raise TypeError(f"positions must be torch.int32 or torch.float32, got {positions.dtype}")
+    if positions.dim() < 2 or positions.shape[-1] != rope.n_axes or not positions.is_contiguous():
+        raise ValueError(f"positions must be a contiguous [tokens, {rope.n_axes}], got {tuple(positions.shape)}")
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    elif q_out.shape != q.shape:
+        raise ValueError(f"q_out must have q's shape {tuple(q.shape)}, got {tuple(q_out.shape)}")
+    _, _, qo_ld, qo_hd = _head_rows(q_out, D, "q_out")
+    a = QkRopeArgs(tokens=tokens, pos_rows=positions.numel() // rope.n_axes, heads=H,
+                   positions_f32=positions.dtype == torch.float32, eps=eps, positions=positions.data_ptr(),
+                   q=q.data_ptr(), q_out=q_out.data_ptr(), q_stride=q_ld, q_head_stride=q_hd, q_out_stride=qo_ld,
+                   q_out_head_stride=qo_hd)
+    if k is not None:
+        tk, a.kv_heads, a.k_stride, a.k_head_stride = _head_rows(k, D, "k")
+        if tk != tokens:
+            raise ValueError(f"k has {tk} tokens, q {tokens}")
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        elif k_out.shape != k.shape:
+            raise ValueError(f"k_out must have k's shape {tuple(k.shape)}, got {tuple(k_out.shape)}")
+        _, _, a.k_out_stride, a.k_out_head_stride = _head_rows(k_out, D, "k_out")
+        a.k, a.k_out = k.data_ptr(), k_out.data_ptr()
+    elif k_out is not None or k_weight is not None:
+        raise ValueError("k_out and k_weight need k")
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            if w.dtype != torch.bfloat16:
+                raise TypeError(f"{name} must be torch.bfloat16, got {w.dtype}")
+            if w.shape != (D,) or not w.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous [{D}], got {tuple(w.shape)}")
+            setattr(a, name, w.data_ptr())
+    _check(load_library().vsa_qk_rope(rope.handle, ctypes.byref(a), _stream(stream)), "vsa_qk_rope")
+    return q_out, k_out
+
+
+# ---------------------------------------------------------------------------
+# Attention over packed whole prompts
+# ---------------------------------------------------------------------------
+
+
+def make_packed_desc(lengths, heads, kv_heads=None, head_dim=128, causal=True, softmax_scale=0.0):
+    """Build the ``vsa_packed_desc`` struct; returns (struct, keep-alive buffer)."""
+    n = [int(x) for x in lengths]
+    if any(x > 0x7fffffff for x in n):
+        raise ValueError("a length is 2^31 or more")
+    buf = (ctypes.c_int32 * max(1, len(n)))(*n)
+    d = PackedDesc(len(n), int(heads), int(heads if kv_heads is None else kv_heads), int(head_dim), int(bool(causal)),
+                   float(softmax_scale), ctypes.cast(buf, ctypes.POINTER(ctypes.c_int32)))
+    return d, buf
+
+
+def vsa_packed_query(lengths, heads, kv_heads=None, head_dim=128, causal=True, softmax_scale=0.0, sms=148) -> dict:
+    """Resolve the sizes of a packed plan without touching a device, with its schedule for a GPU of `sms` SMs:
+    "items" [n, 4] (sequence's first row, its length, the item's first token inside it, key head) and
+    "first" [ctas + 1]."""
+    import numpy as np
+
+    desc, keep = make_packed_desc(lengths, heads, kv_heads, head_dim, causal, softmax_scale)
+    d, lib = PackedDims(), load_library()
+    _check(lib.vsa_packed_query(ctypes.byref(desc), int(sms), ctypes.byref(d), None, None), "vsa_packed_query")
+    items, first = np.zeros((max(1, d.items), 4), np.int32), np.zeros(d.ctas + 1, np.int32)
+    _check(lib.vsa_packed_query(ctypes.byref(desc), int(sms), ctypes.byref(d), items.ctypes.data, first.ctypes.data),
+           "vsa_packed_query")
+    return dict(d.as_dict(), items=items[:d.items], first=first)
+
+
+class PackedPlan:
+    """Owns a ``vsa_packed_plan_t`` handle: the lengths of packed sequences and the schedule made from them."""
+
+    def __init__(self, handle, heads, kv_heads, head_dim, causal):
+        self._h = handle
+        self.heads, self.kv_heads, self.head_dim, self.causal = heads, kv_heads, head_dim, causal
+        d = PackedDims()
+        _check(load_library().vsa_packed_info(self._h, ctypes.byref(d)), "vsa_packed_info")
+        self.dims = d.as_dict()
+
+    @property
+    def handle(self):
+        if self._h is None:
+            raise ValueError("plan destroyed")
+        return self._h
+
+    def status(self, stream=None):
+        """(code, site) of the plan's device status word, (0, 0) unless a device-side wait ran out."""
+        code, where = ctypes.c_int32(), ctypes.c_int32()
+        _check(load_library().vsa_packed_status(self.handle, _stream(stream), ctypes.byref(code), ctypes.byref(where)),
+               "vsa_packed_status")
+        return code.value, where.value
+
+    def destroy(self):
+        if self._h is not None:
+            load_library().vsa_packed_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.destroy()
+        except Exception:
+            pass
+
+
+def vsa_packed_plan(lengths, heads, kv_heads=None, head_dim=128, causal=True, softmax_scale=0.0, stream=None) -> PackedPlan:
+    """A plan for attention over sequences of these lengths packed end to end (0 allowed), for heads query heads
+    and kv_heads key heads (heads / kv_heads query heads share one, in order)."""
+    desc, keep = make_packed_desc(lengths, heads, kv_heads, head_dim, causal, softmax_scale)
+    h = ctypes.c_void_p()
+    _check(load_library().vsa_packed_plan(ctypes.byref(desc), _stream(stream), ctypes.byref(h)), "vsa_packed_plan")
+    return PackedPlan(h, desc.heads, desc.kv_heads, desc.head_dim, bool(causal))
+
+
+def vsa_packed_attn(plan, q, k, v, out=None, stream=None):
+    """softmax(scale q k^T) v of every packed sequence: q [T, H, D], k and v [T, Hk, D] bf16 (any token and head
+    strides that are multiples of 8), T at least the lengths' sum; rows behind the last sequence are left as they
+    are in `out` (zero in an output allocated here)."""
+    D, n = plan.head_dim, plan.dims["tokens"]
+    a = PackedArgs()
+    T, H, a.q_stride, a.q_head_stride = _head_rows(q, D, "q")
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if T > n:
+            out.view(T, H, D)[n:].zero_()
+    _on_device(q.device, q=q, k=k, v=v, out=out)
+    Tk, Hk, a.k_stride, a.k_head_stride = _head_rows(k, D, "k")
+    Tv, Hv, a.v_stride, a.v_head_stride = _head_rows(v, D, "v")
+    if out.shape != q.shape:
+        raise ValueError(f"out must have q's shape {tuple(q.shape)}, got {tuple(out.shape)}")
+    _, _, a.out_stride, a.out_head_stride = _head_rows(out, D, "out")
+    if H != plan.heads or Hk != plan.kv_heads or Hv != plan.kv_heads:
+        raise ValueError(f"the plan has {plan.heads} query and {plan.kv_heads} key heads, got {H}, {Hk} and {Hv}")
+    if Tk != T or Tv != T:
+        raise ValueError(f"q has {T} rows, k {Tk}, v {Tv}")
+    a.tokens, a.q, a.k, a.v, a.out = T, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr()
+    _check(load_library().vsa_packed_attn(plan.handle, ctypes.byref(a), _stream(stream)), "vsa_packed_attn")
+    return out

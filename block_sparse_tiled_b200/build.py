@@ -29,7 +29,7 @@ def sources():
 
 
 def _inputs():
-    return sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + [os.path.join(INCLUDE, "vsa.h"), __file__]
+    return sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))) + [os.path.join(INCLUDE, "vsa.h"), __file__]
 
 
 def up_to_date() -> bool:

@@ -5,17 +5,23 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
+#include <cstdarg>
 #include <cstdio>
 #include <cstring>
 #include <mutex>
+#include <new>
+#include <queue>
 #include <string>
 #include <type_traits>
 #include <vector>
 
 #include "attn_pair_sm100.cuh"
 #include "attn_sm100.cuh"
+#include "packed_attn_sm100.cuh"
 #include "prep_kernels.cuh"
+#include "status.h"
 #include "vsa.h"
 
 #ifndef VSA_PAIR_PREFIX
@@ -30,6 +36,23 @@ vsa_status fail(vsa_status s, const std::string& msg) {
   g_last_error = msg;
   return s;
 }
+
+}  // namespace
+
+vsa_status vsa::set_error(vsa_status s, const char* format, ...) noexcept {
+  char text[256];
+  va_list args;
+  va_start(args, format);
+  std::vsnprintf(text, sizeof text, format, args);
+  va_end(args);
+  try {
+    g_last_error = text;
+  } catch (...) {  // no memory for the message: the status still says what happened
+  }
+  return s;
+}
+
+namespace {
 
 #define VSA_CUDA_TRY(call)                                                                  \
   do {                                                                                      \
@@ -1506,6 +1529,300 @@ vsa_status vsa_wait_selftest(vsa_plan p, int64_t timeout_ns, void* stream, int32
 
 vsa_status vsa_device_status(vsa_plan p, void* stream, int32_t* code, int32_t* where) {
   VSA_TRY(check_plan(p));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int h[2] = {0, 0};
+  VSA_CUDA_TRY(cudaMemcpyAsync(h, p->d_status, sizeof h, cudaMemcpyDeviceToHost, s));
+  VSA_CUDA_TRY(cudaStreamSynchronize(s));
+  VSA_CUDA_TRY(cudaMemsetAsync(p->d_status, 0, sizeof h, s));
+  VSA_CUDA_TRY(cudaStreamSynchronize(s));
+  if (code) *code = h[0];
+  if (where) *where = h[1];
+  return VSA_OK;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- attention over packed prompts
+
+struct vsa_packed_plan_s {
+  int device = 0;
+  int32_t heads = 0, kv_heads = 0, D = 0, causal = 0;
+  vsa_packed_dims dims{};
+  std::vector<vsa::PackedItem> items;
+  std::vector<int32_t> first;
+  void* d_table = nullptr;  // items, first, then the status word (two int32)
+  vsa::PackedItem* d_items = nullptr;
+  int32_t* d_first = nullptr;
+  int* d_status = nullptr;
+};
+
+namespace {
+
+constexpr int64_t kMaxPackedItems = int64_t(1) << 24;
+
+// Sizes and, with items not NULL, the schedule: every (sequence, pair of tiles, key head) is an item whose
+// cost is the key blocks its tiles visit plus kItemCost for what an item costs by itself (its query loads,
+// first scores and epilogue, about two blocks' time); items go longest first to the CTA with the least work
+// so far, so the CTAs finish within about one short item of each other.
+vsa_status packed_schedule(const vsa_packed_desc* d, int sms, vsa_packed_dims* dims, std::vector<vsa::PackedItem>* items,
+                           std::vector<int32_t>* first) {
+  constexpr int64_t kItemCost = 2;
+  if (d == nullptr) return fail(VSA_ERR_INVALID_ARG, "desc is NULL");
+  if (d->n_seqs < 0) return fail(VSA_ERR_INVALID_ARG, "n_seqs < 0");
+  if (d->n_seqs > 0 && d->lengths == nullptr) return fail(VSA_ERR_INVALID_ARG, "lengths is NULL");
+  if (d->heads < 1 || d->kv_heads < 1 || d->heads > 65535)
+    return fail(VSA_ERR_INVALID_ARG, "heads and kv_heads must lie in [1, 65535]");
+  if (d->heads % d->kv_heads != 0) return fail(VSA_ERR_SHAPE, "heads must be a multiple of kv_heads");
+  if (d->causal != 0 && d->causal != 1) return fail(VSA_ERR_INVALID_ARG, "causal must be 0 or 1");
+  if (d->head_dim != 64 && d->head_dim != 96 && d->head_dim != 128)
+    return fail(VSA_ERR_UNSUPPORTED, "head_dim must be 64, 96 or 128, got " + std::to_string(d->head_dim));
+  const int32_t g = d->heads / d->kv_heads;
+  if (g > 128) return fail(VSA_ERR_UNSUPPORTED, "heads / kv_heads must not exceed 128, got " + std::to_string(g));
+  if (sms < 1) return fail(VSA_ERR_INVALID_ARG, "sms must be >= 1");
+  *dims = vsa_packed_dims{};
+  dims->softmax_scale = (d->softmax_scale != 0.0f)
+                            ? d->softmax_scale
+                            : static_cast<float>(1.0 / std::sqrt(static_cast<double>(d->head_dim)));
+  if (!std::isfinite(dims->softmax_scale) || dims->softmax_scale <= 0.0f)
+    return fail(VSA_ERR_INVALID_ARG, "softmax_scale must be > 0");
+  const int64_t tb = 128 / g;
+  dims->tile_tokens = static_cast<int32_t>(tb);
+  for (int32_t s = 0; s < d->n_seqs; ++s) {
+    const int64_t n = d->lengths[s];
+    if (n < 0) return fail(VSA_ERR_INVALID_ARG, "lengths[" + std::to_string(s) + "] is negative");
+    dims->tokens += n;
+    dims->pairs += d->causal ? n * (n + 1) / 2 : n * n;
+    dims->items += (n + 2 * tb - 1) / (2 * tb) * d->kv_heads;
+    if (dims->tokens >= (int64_t(1) << 31) - 1024)
+      return fail(VSA_ERR_UNSUPPORTED, "the lengths' sum must stay below 2^31 - 1024");
+  }
+  if (dims->items > kMaxPackedItems)
+    return fail(VSA_ERR_UNSUPPORTED, "more than 2^24 work items: split the batch");
+  dims->ctas = static_cast<int32_t>(std::min<int64_t>(sms, dims->items));
+  if (items == nullptr) return VSA_OK;
+  struct Costed {
+    int64_t cost;
+    vsa::PackedItem item;
+  };
+  std::vector<Costed> all;
+  all.reserve(static_cast<size_t>(dims->items));
+  int64_t row0 = 0;
+  for (int32_t s = 0; s < d->n_seqs; ++s) {
+    const int64_t n = d->lengths[s];
+    for (int64_t t0 = 0; t0 < n; t0 += 2 * tb) {
+      int64_t cost = kItemCost;
+      for (int64_t t = t0; t < std::min(n, t0 + 2 * tb); t += tb)
+        cost += ((d->causal ? std::min(n, t + tb) : n) + 127) / 128;
+      for (int32_t h = 0; h < d->kv_heads; ++h)
+        all.push_back({cost, vsa::PackedItem{static_cast<int32_t>(row0), static_cast<int32_t>(n), static_cast<int32_t>(t0), h}});
+    }
+    row0 += n;
+  }
+  std::stable_sort(all.begin(), all.end(), [](const Costed& a, const Costed& b) { return a.cost > b.cost; });
+  const int32_t ctas = dims->ctas;
+  std::vector<std::vector<vsa::PackedItem>> lists(static_cast<size_t>(ctas));
+  using Load = std::pair<int64_t, int32_t>;  // work so far, CTA
+  std::priority_queue<Load, std::vector<Load>, std::greater<Load>> least;
+  for (int32_t c = 0; c < ctas; ++c) least.push({0, c});
+  for (const Costed& a : all) {
+    Load l = least.top();
+    least.pop();
+    lists[static_cast<size_t>(l.second)].push_back(a.item);
+    l.first += a.cost;
+    least.push(l);
+  }
+  items->clear();
+  first->assign(1, 0);
+  for (const auto& l : lists) {
+    items->insert(items->end(), l.begin(), l.end());
+    first->push_back(static_cast<int32_t>(items->size()));
+  }
+  return VSA_OK;
+}
+
+// q, k or v [tokens, heads, D] with token and head strides as a 3-D map (d, head, token); a box is 64 columns
+// of `box_heads` heads of `box_tokens` tokens, 128 bytes a row, 128-byte swizzle.  Rows past `tokens` read as
+// zeros.
+vsa_status make_packed_map(CUtensorMap* m, const void* base, int64_t tokens, int64_t heads, int D, int64_t ld,
+                           int64_t hd, int box_heads, int box_tokens) {
+  EncodeTiledFn enc;
+  VSA_TRY(get_encoder(&enc));
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(tokens)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(hd) * 2, static_cast<cuuint64_t>(ld) * 2};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_tokens)};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(VSA_ERR_CUDA, "cuTensorMapEncodeTiled (packed map) failed with code " + std::to_string(r));
+  return VSA_OK;
+}
+
+// Token and head strides of one operand: multiples of 8 elements (16 bytes) below 2^39 (a tensor map's limit
+// is 2^40 bytes).  The output's rows must not overlap.
+vsa_status check_packed_strides(const char* what, int64_t tokens, int64_t heads, int D, int64_t ld, int64_t hd,
+                                bool output) {
+  for (const int64_t x : {ld, hd})
+    if (x < 0 || (x & 7) != 0 || x >= (int64_t(1) << 39))
+      return fail(VSA_ERR_INVALID_ARG, std::string(what) + ": strides must be non-negative multiples of 8 elements");
+  const bool token_major = (heads == 1 || hd >= D) && (tokens == 1 || ld >= (heads - 1) * hd + D);
+  const bool head_major = (tokens == 1 || ld >= D) && (heads == 1 || hd >= (tokens - 1) * ld + D);
+  if (output && !token_major && !head_major) return fail(VSA_ERR_SHAPE, std::string(what) + ": its rows overlap");
+  return VSA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+vsa_status vsa_packed_query(const vsa_packed_desc* d, int32_t sms, vsa_packed_dims* out, int32_t* items,
+                            int32_t* first) {
+  try {
+    if (out == nullptr) return fail(VSA_ERR_INVALID_ARG, "out is NULL");
+    if ((items == nullptr) != (first == nullptr))
+      return fail(VSA_ERR_INVALID_ARG, "items and first must be both NULL or both set");
+    vsa_packed_dims dims;
+    std::vector<vsa::PackedItem> list;
+    std::vector<int32_t> begin;
+    VSA_TRY(packed_schedule(d, sms, &dims, items ? &list : nullptr, &begin));
+    *out = dims;
+    if (items != nullptr) {
+      if (!list.empty()) std::memcpy(items, list.data(), list.size() * sizeof(vsa::PackedItem));
+      std::memcpy(first, begin.data(), begin.size() * sizeof(int32_t));
+    }
+    return VSA_OK;
+  } catch (const std::exception&) {
+    return vsa::set_error(VSA_ERR_INVALID_ARG, "out of host memory");
+  }
+}
+
+vsa_status vsa_packed_plan(const vsa_packed_desc* d, void* stream, vsa_packed_plan_t* out) {
+  vsa_packed_plan_s* p = nullptr;
+  try {
+    if (out == nullptr) return fail(VSA_ERR_INVALID_ARG, "out is NULL");
+    *out = nullptr;
+    vsa_packed_dims dims;
+    VSA_TRY(packed_schedule(d, 1, &dims, nullptr, nullptr));  // the argument checks
+    int dev = 0, major = 0, minor = 0, sms = 0;
+    VSA_CUDA_TRY(cudaGetDevice(&dev));
+    VSA_CUDA_TRY(cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev));
+    VSA_CUDA_TRY(cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev));
+    VSA_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+    if (major != 10 || minor != 0)
+      return fail(VSA_ERR_DEVICE, "libvsa is built for sm_100a; device " + std::to_string(dev) + " is sm_" +
+                                      std::to_string(major) + std::to_string(minor));
+    p = new vsa_packed_plan_s();
+    p->device = dev;
+    p->heads = d->heads;
+    p->kv_heads = d->kv_heads;
+    p->D = d->head_dim;
+    p->causal = d->causal;
+    vsa_status st = packed_schedule(d, sms, &p->dims, &p->items, &p->first);
+    if (st != VSA_OK) {
+      delete p;
+      return st;
+    }
+    const size_t item_bytes = align256(p->items.size() * sizeof(vsa::PackedItem));
+    const size_t first_bytes = align256(p->first.size() * sizeof(int32_t));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaMalloc(&p->d_table, item_bytes + first_bytes + 256);
+    if (e == cudaSuccess) {
+      auto* base = static_cast<uint8_t*>(p->d_table);
+      p->d_items = reinterpret_cast<vsa::PackedItem*>(base);
+      p->d_first = reinterpret_cast<int32_t*>(base + item_bytes);
+      p->d_status = reinterpret_cast<int*>(base + item_bytes + first_bytes);
+      if (!p->items.empty())
+        e = cudaMemcpyAsync(p->d_items, p->items.data(), p->items.size() * sizeof(vsa::PackedItem),
+                            cudaMemcpyHostToDevice, s);
+      if (e == cudaSuccess)
+        e = cudaMemcpyAsync(p->d_first, p->first.data(), p->first.size() * sizeof(int32_t), cudaMemcpyHostToDevice, s);
+      if (e == cudaSuccess) e = cudaMemsetAsync(p->d_status, 0, 2 * sizeof(int), s);
+      // calls may come on other streams than this one: the table is there when the plan is
+      if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    }
+    if (e != cudaSuccess) {
+      cudaFree(p->d_table);
+      delete p;
+      return fail(VSA_ERR_CUDA, std::string("packed plan upload: ") + cudaGetErrorString(e));
+    }
+    *out = p;
+    return VSA_OK;
+  } catch (const std::exception&) {
+    delete p;
+    return vsa::set_error(VSA_ERR_INVALID_ARG, "out of host memory");
+  }
+}
+
+vsa_status vsa_packed_info(vsa_packed_plan_t p, vsa_packed_dims* out) {
+  if (p == nullptr || out == nullptr) return vsa::set_error(VSA_ERR_INVALID_ARG, "NULL argument");
+  *out = p->dims;
+  return VSA_OK;
+}
+
+vsa_status vsa_packed_destroy(vsa_packed_plan_t p) {
+  if (p == nullptr) return VSA_OK;
+  int prev = -1;
+  cudaGetDevice(&prev);
+  cudaSetDevice(p->device);
+  cudaDeviceSynchronize();
+  cudaFree(p->d_table);
+  if (prev >= 0) cudaSetDevice(prev);
+  delete p;
+  return VSA_OK;
+}
+
+vsa_status vsa_packed_attn(vsa_packed_plan_t p, const vsa_packed_args* a, void* stream) {
+  try {
+    if (p == nullptr) return fail(VSA_ERR_INVALID_ARG, "plan is NULL");
+    if (a == nullptr) return fail(VSA_ERR_INVALID_ARG, "args is NULL");
+    int dev = -1;
+    VSA_CUDA_TRY(cudaGetDevice(&dev));
+    if (dev != p->device) return fail(VSA_ERR_INVALID_ARG, "the current device is not the plan's device");
+    if (a->tokens < p->dims.tokens)
+      return fail(VSA_ERR_SHAPE, "tokens is " + std::to_string(a->tokens) + ", the plan's sequences hold " +
+                                     std::to_string(p->dims.tokens));
+    if (p->dims.items == 0) return VSA_OK;
+    VSA_TRY(check_ptrs({a->q, a->k, a->v, a->out}));
+    const int64_t n = p->dims.tokens;
+    VSA_TRY(check_packed_strides("q", n, p->heads, p->D, a->q_stride, a->q_head_stride, false));
+    VSA_TRY(check_packed_strides("k", n, p->kv_heads, p->D, a->k_stride, a->k_head_stride, false));
+    VSA_TRY(check_packed_strides("v", n, p->kv_heads, p->D, a->v_stride, a->v_head_stride, false));
+    VSA_TRY(check_packed_strides("out", n, p->heads, p->D, a->out_stride, a->out_head_stride, true));
+    const int g = p->heads / p->kv_heads, tb = p->dims.tile_tokens;
+    CUtensorMap mq, mk, mv;
+    VSA_TRY(make_packed_map(&mq, a->q, n, p->heads, p->D, a->q_stride, a->q_head_stride, g, tb));
+    VSA_TRY(make_packed_map(&mk, a->k, n, p->kv_heads, p->D, a->k_stride, a->k_head_stride, 1, 128));
+    VSA_TRY(make_packed_map(&mv, a->v, n, p->kv_heads, p->D, a->v_stride, a->v_head_stride, 1, 128));
+    vsa::PackedArgs k{};
+    k.items = p->d_items;
+    k.first = p->d_first;
+    k.out = a->out;
+    k.out_ld = a->out_stride;
+    k.out_hd = a->out_head_stride;
+    k.status = p->d_status;
+    k.group = g;
+    k.tile_tokens = tb;
+    k.causal = p->causal;
+    k.scale_log2 = static_cast<float>(static_cast<double>(p->dims.softmax_scale) * 1.4426950408889634);
+    return with_head_dim(p->D, [&](auto dc) -> vsa_status {
+      constexpr int D = decltype(dc)::value;
+      const size_t smem = vsa::PackedLayout<D>::bytes();
+      VSA_TRY(allow_smem(vsa::packed_attn_kernel<D>, smem));
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(static_cast<unsigned>(p->dims.ctas));
+      cfg.blockDim = dim3(vsa::kPackedThreads);
+      cfg.dynamicSmemBytes = smem;
+      cfg.stream = static_cast<cudaStream_t>(stream);
+      VSA_CUDA_TRY(cudaLaunchKernelEx(&cfg, vsa::packed_attn_kernel<D>, mq, mk, mv, k));
+      return VSA_OK;
+    });
+  } catch (const std::exception&) {
+    return vsa::set_error(VSA_ERR_INVALID_ARG, "out of host memory");
+  }
+}
+
+vsa_status vsa_packed_status(vsa_packed_plan_t p, void* stream, int32_t* code, int32_t* where) {
+  if (p == nullptr) return vsa::set_error(VSA_ERR_INVALID_ARG, "plan is NULL");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int h[2] = {0, 0};
   VSA_CUDA_TRY(cudaMemcpyAsync(h, p->d_status, sizeof h, cudaMemcpyDeviceToHost, s));

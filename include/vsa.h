@@ -404,6 +404,162 @@ typedef struct vsa_workspace_layout {
 } vsa_workspace_layout;
 vsa_status vsa_plan_workspace(vsa_plan p, vsa_workspace_layout* out);
 
+/* ---- row operators around the attention ------------------------------------
+ * Root-mean-square norm with the residual's addition.  For every row, with
+ * t = x + residual in binary32 (t = x without a residual):
+ *   residual_out = t rounded to the residual's type (NULL: not written)
+ *   y            = t * (1 / sqrt(mean(t^2) + eps)) * weight
+ *   out          = y rounded to bf16, or with out_e4m3 the OCP FP8 E4M3 codes
+ *                  of y / scale with scale = max|y| / 448 for each row (the
+ *                  scale rule of qk_fp8; a row of zeros has scale 0 and zero
+ *                  codes; round to nearest even, saturating).  y itself is not
+ *                  rounded before the division, which is carried out in binary32.
+ * The mean is that of the unrounded t, held in binary32.  A row with a NaN or
+ * an infinity gives NaN outputs (with out_e4m3: a NaN scale).
+ *  - width: a multiple of 8 in [8, 16384]; any number of rows, 0 included.
+ *  - strides: elements between rows, multiples of 8; an input's may be 0 (one
+ *    row for all) or any, an output's at least the width.
+ *  - In place: out may be x, residual_out may be residual or x (same type and
+ *    stride); otherwise outputs must not overlap inputs or one another.
+ * No plan and no workspace: calls on different streams may overlap, and a call
+ * may be captured.  The current device must be the one that holds the tensors.
+ * Errors: VSA_ERR_INVALID_ARG, VSA_ERR_SHAPE, VSA_ERR_UNSUPPORTED, VSA_ERR_CUDA. */
+typedef struct vsa_rms_norm_args {
+  int64_t rows;
+  int32_t width;
+  int32_t residual_f32; /* residual and residual_out are 0: bf16, 1: binary32 */
+  int32_t weight_f32;   /* weight is 0: bf16, 1: binary32 */
+  int32_t out_e4m3;     /* out is 0: bf16, 1: E4M3 codes (one byte each) with scale [rows] */
+  float eps;
+  const vsa_bf16* x;
+  const void* residual; /* NULL: none */
+  const void* weight;   /* [width]; NULL: ones */
+  void* out;
+  void* residual_out;
+  float* scale; /* [rows] with out_e4m3 */
+  int64_t x_stride, residual_stride, out_stride, residual_out_stride;
+} vsa_rms_norm_args;
+vsa_status vsa_rms_norm(const vsa_rms_norm_args* args, void* stream);
+
+/* Rotary positions with several axes (time, height, width, ...), and the
+ * per-head norm of Q and K in the same pass ("FastH3 NVFP4 on RTX PRO 6000
+ * (sm_120)", section "Model integration": QK-norm, then RoPE, before the
+ * attention).  A vsa_rope holds, for every pair p < head_dim / 2 of a head row,
+ * a frequency f_p and the axis a_p whose position it follows:
+ *   - sections[n_axes] pairs in a row per axis (time's first, then height's ..);
+ *     pairs behind the last section do not turn (f = 0);
+ *   - f of the i-th of the n pairs of an axis is theta^(-i / n), or with
+ *     shared_ladder theta^(-p / (head_dim / 2)) for pair p of the head;
+ *   - or, with inv_freq and axis [head_dim / 2] given, any table (sections and
+ *     theta are then not read).
+ * Pair p is elements (p, p + head_dim / 2), or (2p, 2p + 1) with interleaved.
+ * A vsa_rope lives on the host, is never changed and may be used by any number
+ * of calls, streams and devices at once; destroy it after the last call. */
+typedef struct vsa_rope_desc {
+  int32_t head_dim; /* 64, 96 or 128 */
+  int32_t n_axes;   /* 1..4 */
+  int32_t interleaved, shared_ladder;
+  const int32_t* sections;
+  double theta;
+  const double* inv_freq; /* radians per position step; NULL: from sections */
+  const int32_t* axis;
+} vsa_rope_desc;
+typedef struct vsa_rope_s* vsa_rope;
+vsa_status vsa_rope_create(const vsa_rope_desc* desc, vsa_rope* out);
+/* inv_freq[head_dim / 2] and axis[head_dim / 2] of every pair (either may be NULL). */
+vsa_status vsa_rope_table(vsa_rope r, double* inv_freq, int32_t* axis);
+vsa_status vsa_rope_destroy(vsa_rope r);
+
+/* For every token and head of q (and of k when kv_heads > 0), in binary32 with
+ * one rounding to bf16 at the end: with a weight [head_dim] first
+ * y = x * (1 / sqrt(mean(x^2) + eps)) * weight over the head row (y = x without),
+ * then each pair (a, b) turns by angle = position * f_p:
+ *   (a cos - b sin, a sin + b cos).
+ * positions: [pos_rows, n_axes], int32 or binary32; token t uses row
+ * t % pos_rows (pos_rows = L serves a [B, L, ..] batch).  The angle is the
+ * binary64 product reduced in binary64, so far positions keep their accuracy.
+ *  - strides: elements between tokens and between heads, multiples of 8, so q
+ *    and k may be slices of one projection; output rows must not overlap.
+ *  - In place: q_out may be q and k_out may be k (same strides); otherwise
+ *    outputs must not overlap inputs.
+ * No workspace: calls may overlap on the GPU and may be captured.  The current
+ * device must be the one that holds the tensors.
+ * Errors: VSA_ERR_INVALID_ARG, VSA_ERR_SHAPE, VSA_ERR_CUDA. */
+typedef struct vsa_qk_rope_args {
+  int64_t tokens;
+  int64_t pos_rows;
+  int32_t heads, kv_heads;
+  int32_t positions_f32; /* positions are 0: int32, 1: binary32 */
+  float eps;
+  const void* positions;
+  const vsa_bf16 *q, *k;
+  vsa_bf16 *q_out, *k_out;
+  const vsa_bf16 *q_weight, *k_weight; /* [head_dim]; NULL: no head norm */
+  int64_t q_stride, q_head_stride, k_stride, k_head_stride;
+  int64_t q_out_stride, q_out_head_stride, k_out_stride, k_out_head_stride;
+} vsa_qk_rope_args;
+vsa_status vsa_qk_rope(vsa_rope r, const vsa_qk_rope_args* args, void* stream);
+
+/* ---- attention over packed whole prompts ------------------------------------
+ * Dense attention of sequences of different lengths packed end to end, as the
+ * text model that supplies the prefix runs it: for token i of a sequence and
+ * query head h, over the keys j of the same sequence (with causal: j <= i),
+ *   out[i, h] = sum_j softmax_j(softmax_scale * q[i, h] . k[j, h / g]) v[j, h / g],
+ * g = heads / kv_heads.  bf16 in and out, binary32 scores, maxima and sums, P
+ * rounded to bf16 for the P.V product (as vsa_sparse_attn_fwd).
+ *  - A plan holds the lengths (0 allowed) and the schedule made from them; it
+ *    owns a small device table, uploaded on `stream` to the current device, and
+ *    a status word.  Calls with one plan may overlap on the GPU (nothing in it
+ *    is written but the status word of a failed wait) and may be captured;
+ *    the plan must live until they, and the graphs that hold them, are done.
+ *    Create it outside of a capture.
+ *  - q, out [tokens, heads, head_dim], k, v [tokens, kv_heads, head_dim] with
+ *    any token and head strides that are multiples of 8 elements; tokens >=
+ *    the lengths' sum.  Rows behind the last sequence are neither read nor
+ *    written.
+ *  - A sequence's output depends on its own rows only, whatever the others
+ *    hold.  Inside one, a masked key's score is replaced, so NaN or infinite
+ *    keys stay where they are seen; a NaN or infinite value v[j] may also reach
+ *    masked rows i < j of its own sequence (0 * NaN in the P.V product).
+ * Errors: VSA_ERR_INVALID_ARG, VSA_ERR_SHAPE, VSA_ERR_UNSUPPORTED,
+ * VSA_ERR_DEVICE, VSA_ERR_CUDA; a wait that ran out on the device is in the
+ * plan's status word (vsa_packed_status). */
+typedef struct vsa_packed_desc {
+  int32_t n_seqs;
+  int32_t heads, kv_heads; /* heads a multiple of kv_heads, heads / kv_heads <= 128 */
+  int32_t head_dim;        /* 64, 96 or 128 */
+  int32_t causal;
+  float softmax_scale;    /* 0 => (float)(1 / sqrt((double)head_dim)) */
+  const int32_t* lengths; /* [n_seqs], host; read only during vsa_packed_plan */
+} vsa_packed_desc;
+typedef struct vsa_packed_plan_s* vsa_packed_plan_t;
+typedef struct vsa_packed_dims {
+  int64_t tokens;        /* sum of the lengths */
+  int64_t pairs;         /* (query, key) pairs per query head */
+  int64_t items;         /* work items: up to two tiles of 128 query rows of one key head */
+  int32_t ctas;          /* persistent CTAs they are spread over */
+  int32_t tile_tokens;   /* tokens per tile: floor(128 / (heads / kv_heads)) */
+  float softmax_scale;   /* the scale actually used */
+} vsa_packed_dims;
+vsa_status vsa_packed_plan(const vsa_packed_desc* desc, void* stream, vsa_packed_plan_t* out);
+/* Sizes without a device; sms: the GPU's SM count the schedule is made for (148 on a B200).  With items
+ * not NULL, also the schedule: items[4 * items] = (sequence's first row, its length, the item's first token
+ * inside it, key head) in the order of the CTAs, first[ctas + 1] = where each CTA's begin. */
+vsa_status vsa_packed_query(const vsa_packed_desc* desc, int32_t sms, vsa_packed_dims* out, int32_t* items,
+                            int32_t* first);
+vsa_status vsa_packed_info(vsa_packed_plan_t p, vsa_packed_dims* out);
+vsa_status vsa_packed_destroy(vsa_packed_plan_t p); /* synchronises with the device first */
+typedef struct vsa_packed_args {
+  int64_t tokens; /* rows of q, k, v and out, >= the plan's tokens */
+  const vsa_bf16 *q, *k, *v;
+  vsa_bf16* out;
+  int64_t q_stride, q_head_stride, k_stride, k_head_stride;
+  int64_t v_stride, v_head_stride, out_stride, out_head_stride;
+} vsa_packed_args;
+vsa_status vsa_packed_attn(vsa_packed_plan_t p, const vsa_packed_args* args, void* stream);
+/* Read (synchronising `stream`) and clear the plan's device status word, as vsa_device_status. */
+vsa_status vsa_packed_status(vsa_packed_plan_t p, void* stream, int32_t* code, int32_t* where);
+
 /* Failure-detection self-test.  No counterpart on the pages: it checks the
  * library's own safety net.  It launches one small kernel whose threads wait,
  * with the same bounded-wait code the attention kernel uses, on a barrier that
