@@ -603,30 +603,49 @@ def workspace_views(plan, workspace):
 # ---------------------------------------------------------------------------
 
 
-def _on_device(device, **tensors):
-    """Every given tensor is a CUDA tensor of `device`, and that is the current device (the library launches
-    on the current device, in its current stream unless one is given)."""
-    for name, t in tensors.items():
+_BF16, _F32, _E4M3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+
+
+def _launch_index(names, *tensors):
+    """The index of the one CUDA device that holds every given tensor, which must be the current device (the
+    library launches there).  These calls are a few microseconds of GPU work at their smallest, so the checks
+    go by index and build nothing."""
+    index = None
+    for t in tensors:
         if t is None:
             continue
         if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if t.device != device or device.type != "cuda":
+            raise TypeError(f"{names[tensors.index(t)]} must be a torch.Tensor")
+        i = t.get_device()
+        if index is None:
+            index = i
+        if i < 0 or i != index:
+            name = next(n for n, x in zip(names, tensors) if x is t)
             raise ValueError(f"{name} is on {t.device}: every tensor must be on one CUDA device")
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+    if index != torch._C._cuda_getDevice():
+        raise ValueError(f"the tensors are on cuda:{index}, the current device is cuda:{torch.cuda.current_device()}")
+    return index
 
 
-def _rows(t, width, name):
-    """(rows, elements between rows) of a tensor whose last dimension is `width`: two-dimensional with unit
-    stride inside its rows, or contiguous."""
-    if t.dim() < 1 or t.shape[-1] != width:
-        raise ValueError(f"{name} must end in a dimension of {width}, got shape {tuple(t.shape)}")
-    if t.dim() == 2 and t.stride(1) == 1:
-        return t.shape[0], (t.stride(0) if t.shape[0] > 1 else width)
+def _stream_on(stream, index):
+    """The raw handle of `stream`, by default the current stream of device `index`."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _row_stride(t, shape, name):
+    """Elements between rows of a tensor of this shape: two-dimensional with unit stride inside its rows, or
+    contiguous."""
+    if t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
+    if len(shape) == 2:
+        s = t.stride()
+        if s[1] == 1:
+            return s[0] if shape[0] > 1 else shape[1]
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous, or two-dimensional with contiguous rows")
-    return t.numel() // width, width
+    return shape[-1]
 
 
 def vsa_rms_norm(x, weight=None, eps=1e-6, residual=None, out=None, residual_out=None, scale=None, out_dtype=None,
@@ -639,61 +658,57 @@ def vsa_rms_norm(x, weight=None, eps=1e-6, residual=None, out=None, residual_out
     float32 scale per row, scale = max|y| / 448 (out.float() * scale[..., None] is y, rounded).
     residual_out receives x + residual in the residual's type (allocated when there is a residual; the residual
     itself may be passed, and out may be x).  Returns (out, scale or None, residual_out or None)."""
-    _on_device(x.device, x=x, weight=weight, residual=residual, out=out, residual_out=residual_out, scale=scale)
-    if x.dtype != torch.bfloat16:
+    index = _launch_index(("x", "weight", "residual", "out", "residual_out", "scale"), x, weight, residual, out,
+                          residual_out, scale)
+    if x.dtype != _BF16:
         raise TypeError(f"x must be torch.bfloat16, got {x.dtype}")
-    if x.dim() < 1:
-        raise ValueError("x must have at least one dimension")
-    C = x.shape[-1]
+    shape = x.shape
+    if not shape or shape[-1] == 0:
+        raise ValueError(f"x must end in a dimension that is not empty, got {tuple(shape)}")
+    C = shape[-1]
+    rows = x.numel() // C
     if out is None:
-        out = torch.empty(x.shape, dtype=out_dtype or torch.bfloat16, device=x.device)
+        out = torch.empty(shape, dtype=out_dtype or _BF16, device=x.device)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out is {out.dtype}, out_dtype is {out_dtype}")
-    if out.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+    f8 = out.dtype == _E4M3
+    if not f8 and out.dtype != _BF16:
         raise TypeError(f"the output type must be torch.bfloat16 or torch.float8_e4m3fn, got {out.dtype}")
-    f8 = out.dtype == torch.float8_e4m3fn
-    if C == 0:
-        raise ValueError("the last dimension of x is empty")
-    rows, x_ld = _rows(x, C, "x")
-    a = RmsNormArgs(rows=rows, width=C, out_e4m3=f8, eps=eps, x=x.data_ptr(), out=out.data_ptr(), x_stride=x_ld)
-    if out.shape != x.shape:
-        raise ValueError(f"out must have x's shape {tuple(x.shape)}, got {tuple(out.shape)}")
-    a.out_stride = _rows(out, C, "out")[1]
+    w_ptr = w_f32 = s_ptr = r_ptr = ro_ptr = r_f32 = r_ld = ro_ld = 0
     if weight is not None:
-        if weight.dtype not in (torch.bfloat16, torch.float32):
+        w_f32 = weight.dtype == _F32
+        if not w_f32 and weight.dtype != _BF16:
             raise TypeError(f"weight must be torch.bfloat16 or torch.float32, got {weight.dtype}")
         if weight.shape != (C,) or not weight.is_contiguous():
             raise ValueError(f"weight must be a contiguous [{C}], got {tuple(weight.shape)}")
-        a.weight, a.weight_f32 = weight.data_ptr(), weight.dtype == torch.float32
+        w_ptr = weight.data_ptr()
     if f8:
         if scale is None:
-            scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-        if scale.dtype != torch.float32:
+            scale = torch.empty(shape[:-1], dtype=_F32, device=x.device)
+        elif scale.dtype != _F32:
             raise TypeError(f"scale must be torch.float32, got {scale.dtype}")
-        if scale.numel() != rows or not scale.is_contiguous():
+        elif scale.numel() != rows or not scale.is_contiguous():
             raise ValueError(f"scale must be contiguous with one value for each of the {rows} rows")
-        a.scale = scale.data_ptr()
+        s_ptr = scale.data_ptr()
     elif scale is not None:
         raise ValueError("scale belongs to an 8-bit output")
-    if residual is None:
-        if residual_out is not None:
-            raise ValueError("residual_out needs a residual")
-    else:
-        if residual.dtype not in (torch.bfloat16, torch.float32):
+    if residual is not None:
+        r_f32 = residual.dtype == _F32
+        if not r_f32 and residual.dtype != _BF16:
             raise TypeError(f"residual must be torch.bfloat16 or torch.float32, got {residual.dtype}")
-        if residual.shape != x.shape:
-            raise ValueError(f"residual must have x's shape {tuple(x.shape)}, got {tuple(residual.shape)}")
         if residual_out is None:
-            residual_out = torch.empty(x.shape, dtype=residual.dtype, device=x.device)
-        if residual_out.dtype != residual.dtype:
+            residual_out = torch.empty(shape, dtype=residual.dtype, device=x.device)
+        elif residual_out.dtype != residual.dtype:
             raise TypeError(f"residual_out must be {residual.dtype}, got {residual_out.dtype}")
-        if residual_out.shape != x.shape:
-            raise ValueError(f"residual_out must have x's shape {tuple(x.shape)}, got {tuple(residual_out.shape)}")
-        a.residual, a.residual_f32 = residual.data_ptr(), residual.dtype == torch.float32
-        a.residual_out = residual_out.data_ptr()
-        a.residual_stride = _rows(residual, C, "residual")[1]
-        a.residual_out_stride = _rows(residual_out, C, "residual_out")[1]
-    _check(load_library().vsa_rms_norm(ctypes.byref(a), _stream(stream)), "vsa_rms_norm")
+        r_ptr, r_ld = residual.data_ptr(), _row_stride(residual, shape, "residual")
+        ro_ptr, ro_ld = residual_out.data_ptr(), _row_stride(residual_out, shape, "residual_out")
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    a = RmsNormArgs(rows, C, r_f32, w_f32, f8, eps, x.data_ptr(), r_ptr, w_ptr, out.data_ptr(), ro_ptr, s_ptr,
+                    _row_stride(x, shape, "x"), r_ld, _row_stride(out, shape, "out"), ro_ld)
+    rc = (_lib or load_library()).vsa_rms_norm(ctypes.byref(a), _stream_on(stream, index))
+    if rc:
+        _check(rc, "vsa_rms_norm")
     return out, scale, residual_out
 
 
@@ -767,23 +782,28 @@ def vsa_rope_create(head_dim, sections=None, theta=10000.0, interleaved=False, s
 def _head_rows(t, D, name):
     """(tokens, heads, elements between tokens, between heads) of [T, H, D], or of [B, L, H, D] whose tokens are
     evenly spaced."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype != _BF16:
         raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.dim() not in (3, 4) or t.shape[-1] != D:
-        raise ValueError(f"{name} must be [T, H, {D}] or [B, L, H, {D}], got {tuple(t.shape)}")
     sh, st = t.shape, t.stride()
+    if len(sh) not in (3, 4) or sh[-1] != D:
+        raise ValueError(f"{name} must be [T, H, {D}] or [B, L, H, {D}], got {tuple(sh)}")
     if st[-1] != 1:
         raise ValueError(f"{name} must have contiguous head rows")
-    tokens, ld = sh[-3], st[-3]
-    if t.dim() == 4:
+    H = sh[-2]
+    tokens, ld, hd = sh[-3], st[-3], (st[-2] if H > 1 else D)
+    if len(sh) == 4:
         if sh[0] > 1 and sh[1] > 1 and st[0] != sh[1] * st[1]:
             raise ValueError(f"{name}: the tokens of [B, L, H, D] must be evenly spaced")
         tokens, ld = sh[0] * sh[1], (st[1] if sh[1] > 1 else st[0])
-    H = sh[-2]
-    hd = st[-2] if H > 1 else D
     return tokens, H, (ld if tokens > 1 else H * D), hd
+
+
+def _head_weight(w, D, name):
+    if w.dtype != _BF16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {w.dtype}")
+    if w.shape != (D,) or not w.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous [{D}], got {tuple(w.shape)}")
+    return w.data_ptr()
 
 
 def vsa_qk_rope(rope, q, k, positions, q_weight=None, k_weight=None, eps=1e-6, q_out=None, k_out=None, stream=None):
@@ -791,42 +811,40 @@ def vsa_qk_rope(rope, q, k, positions, q_weight=None, k_weight=None, eps=1e-6, q
     [B, L, H, D]; any token and head strides that are multiples of 8, e.g. slices of one projection; k may be
     None), bf16.  positions: [T, n_axes] int32 or float32, or [L, n_axes] for a batch of B sequences.  In place
     with q_out = q, k_out = k.  Returns (q_out, k_out)."""
-    D = rope.head_dim
+    D, axes = rope.head_dim, rope.n_axes
+    index = _launch_index(("q", "k", "positions", "q_weight", "k_weight", "q_out", "k_out"), q, k, positions, q_weight,
+                          k_weight, q_out, k_out)
     tokens, H, q_ld, q_hd = _head_rows(q, D, "q")
-    _on_device(q.device, q=q, k=k, positions=positions, q_weight=q_weight, k_weight=k_weight, q_out=q_out, k_out=k_out)
-    if positions.dtype not in (torch.int32, torch.float32):
+    pos_f32 = positions.dtype == _F32
+    if not pos_f32 and positions.dtype != torch.int32:
         raise TypeError(f"positions must be torch.int32 or torch.float32, got {positions.dtype}")
-    if positions.dim() < 2 or positions.shape[-1] != rope.n_axes or not positions.is_contiguous():
-        raise ValueError(f"positions must be a contiguous [tokens, {rope.n_axes}], got {tuple(positions.shape)}")
+    if positions.dim() < 2 or positions.shape[-1] != axes or not positions.is_contiguous():
+        raise ValueError(f"positions must be a contiguous [tokens, {axes}], got {tuple(positions.shape)}")
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        q_out = torch.empty(q.shape, dtype=_BF16, device=q.device)
     elif q_out.shape != q.shape:
         raise ValueError(f"q_out must have q's shape {tuple(q.shape)}, got {tuple(q_out.shape)}")
     _, _, qo_ld, qo_hd = _head_rows(q_out, D, "q_out")
-    a = QkRopeArgs(tokens=tokens, pos_rows=positions.numel() // rope.n_axes, heads=H,
-                   positions_f32=positions.dtype == torch.float32, eps=eps, positions=positions.data_ptr(),
-                   q=q.data_ptr(), q_out=q_out.data_ptr(), q_stride=q_ld, q_head_stride=q_hd, q_out_stride=qo_ld,
-                   q_out_head_stride=qo_hd)
+    Hk = k_ptr = ko_ptr = k_ld = k_hd = ko_ld = ko_hd = 0
     if k is not None:
-        tk, a.kv_heads, a.k_stride, a.k_head_stride = _head_rows(k, D, "k")
+        tk, Hk, k_ld, k_hd = _head_rows(k, D, "k")
         if tk != tokens:
             raise ValueError(f"k has {tk} tokens, q {tokens}")
         if k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+            k_out = torch.empty(k.shape, dtype=_BF16, device=k.device)
         elif k_out.shape != k.shape:
             raise ValueError(f"k_out must have k's shape {tuple(k.shape)}, got {tuple(k_out.shape)}")
-        _, _, a.k_out_stride, a.k_out_head_stride = _head_rows(k_out, D, "k_out")
-        a.k, a.k_out = k.data_ptr(), k_out.data_ptr()
+        _, _, ko_ld, ko_hd = _head_rows(k_out, D, "k_out")
+        k_ptr, ko_ptr = k.data_ptr(), k_out.data_ptr()
     elif k_out is not None or k_weight is not None:
         raise ValueError("k_out and k_weight need k")
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            if w.dtype != torch.bfloat16:
-                raise TypeError(f"{name} must be torch.bfloat16, got {w.dtype}")
-            if w.shape != (D,) or not w.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous [{D}], got {tuple(w.shape)}")
-            setattr(a, name, w.data_ptr())
-    _check(load_library().vsa_qk_rope(rope.handle, ctypes.byref(a), _stream(stream)), "vsa_qk_rope")
+    a = QkRopeArgs(tokens, positions.numel() // axes, H, Hk, pos_f32, eps, positions.data_ptr(), q.data_ptr(), k_ptr,
+                   q_out.data_ptr(), ko_ptr, 0 if q_weight is None else _head_weight(q_weight, D, "q_weight"),
+                   0 if k_weight is None else _head_weight(k_weight, D, "k_weight"), q_ld, q_hd, k_ld, k_hd, qo_ld,
+                   qo_hd, ko_ld, ko_hd)
+    rc = (_lib or load_library()).vsa_qk_rope(rope.handle, ctypes.byref(a), _stream_on(stream, index))
+    if rc:
+        _check(rc, "vsa_qk_rope")
     return q_out, k_out
 
 
@@ -909,23 +927,25 @@ def vsa_packed_attn(plan, q, k, v, out=None, stream=None):
     """softmax(scale q k^T) v of every packed sequence: q [T, H, D], k and v [T, Hk, D] bf16 (any token and head
     strides that are multiples of 8), T at least the lengths' sum; rows behind the last sequence are left as they
     are in `out` (zero in an output allocated here)."""
+    index = _launch_index(("q", "k", "v", "out"), q, k, v, out)
     D, n = plan.head_dim, plan.dims["tokens"]
-    a = PackedArgs()
-    T, H, a.q_stride, a.q_head_stride = _head_rows(q, D, "q")
-    if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if T > n:
-            out.view(T, H, D)[n:].zero_()
-    _on_device(q.device, q=q, k=k, v=v, out=out)
-    Tk, Hk, a.k_stride, a.k_head_stride = _head_rows(k, D, "k")
-    Tv, Hv, a.v_stride, a.v_head_stride = _head_rows(v, D, "v")
-    if out.shape != q.shape:
-        raise ValueError(f"out must have q's shape {tuple(q.shape)}, got {tuple(out.shape)}")
-    _, _, a.out_stride, a.out_head_stride = _head_rows(out, D, "out")
-    if H != plan.heads or Hk != plan.kv_heads or Hv != plan.kv_heads:
+    T, H, q_ld, q_hd = _head_rows(q, D, "q")
+    Tk, Hk, k_ld, k_hd = _head_rows(k, D, "k")
+    Tv, Hv, v_ld, v_hd = _head_rows(v, D, "v")
+    if H != plan.heads or Hk != plan.kv_heads or Hv != Hk:
         raise ValueError(f"the plan has {plan.heads} query and {plan.kv_heads} key heads, got {H}, {Hk} and {Hv}")
     if Tk != T or Tv != T:
         raise ValueError(f"q has {T} rows, k {Tk}, v {Tv}")
-    a.tokens, a.q, a.k, a.v, a.out = T, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr()
-    _check(load_library().vsa_packed_attn(plan.handle, ctypes.byref(a), _stream(stream)), "vsa_packed_attn")
+    if out is None:
+        out = torch.empty(q.shape, dtype=_BF16, device=q.device)
+        if T > n:
+            out.view(T, H, D)[n:].zero_()
+    elif out.shape != q.shape:
+        raise ValueError(f"out must have q's shape {tuple(q.shape)}, got {tuple(out.shape)}")
+    _, _, o_ld, o_hd = _head_rows(out, D, "out")
+    a = PackedArgs(T, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), q_ld, q_hd, k_ld, k_hd, v_ld, v_hd,
+                   o_ld, o_hd)
+    rc = (_lib or load_library()).vsa_packed_attn(plan.handle, ctypes.byref(a), _stream_on(stream, index))
+    if rc:
+        _check(rc, "vsa_packed_attn")
     return out

@@ -57,6 +57,7 @@ struct PackedArgs {
 
 constexpr int kPackedThreads = 384;
 constexpr float kPackedRescale = 8.0f;
+constexpr int kPolyPairs = 1;  // of every four pairs of exponentials, those on the FMA pipe
 constexpr uint32_t kPackedS = 0, kPackedO = 256;  // TMEM columns: S_A, S_B, O_A, O_B, 128 each
 
 template <int D>
@@ -83,6 +84,46 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, uint64_
       : "memory");
 }
 
+// One thread of a converged warp, the same at every call.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(p));
+  return p != 0;
+}
+
+// Shared-memory descriptor in two words (as umma_desc_sw128): the low one moves with the address, the high one
+// is a constant; 1 KB between 8-row groups, `lbo` bytes between the 64-column halves of a K-major step's
+// operand (unused) or of an MN-major operand.
+__device__ __forceinline__ uint32_t umma_desc_lo(uint32_t saddr) { return (saddr & 0x3FFFFu) >> 4; }
+__device__ __forceinline__ uint64_t umma_desc(uint32_t lo, uint32_t lbo) {
+  const uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);
+  return (static_cast<uint64_t>(hi) << 32) | lo | ((lbo >> 4) << 16);
+}
+
+// 2^x of two values with the FMA pipe: 2^floor(x) times a degree-4 polynomial in the remaining fraction
+// (least largest relative error on [0, 1] with p(0) = 1, by linear programming: 3.0e-6 evaluated in binary32).
+// x <= -127 gives exactly 0, so a weight that has vanished stays exactly nothing; x must stay below 127.
+__device__ __forceinline__ void ex2_poly2(float& x0, float& x1) {
+  constexpr float kFloor = 12582912.0f;  // 1.5 * 2^23: adding it, rounded down, leaves floor(x) in the low bits
+  const float a0 = fmaxf(x0, -127.0f), a1 = fmaxf(x1, -127.0f);
+  float t0, t1, f0, f1, p0, p1;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %4};\n\t"
+      "add.rm.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(t0), "=f"(t1)
+      : "f"(a0), "f"(a1), "f"(kFloor));
+  add2(f0, f1, t0, t1, -kFloor, -kFloor);
+  fma2(f0, f1, f0, f1, -1.0f, -1.0f, a0, a1);
+  fma2(p0, p1, f0, f1, 0.013427376f, 0.013427376f, 0.052241072f, 0.052241072f);
+  fma2(p0, p1, p0, p1, f0, f1, 0.24128109f, 0.24128109f);
+  fma2(p0, p1, p0, p1, f0, f1, 0.69304466f, 0.69304466f);
+  fma2(p0, p1, p0, p1, f0, f1, 1.0f, 1.0f);
+  x0 = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(t0) << 23));
+  x1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23));
+}
+
 // What every role derives from an item: the keys each tile can see (0: the tile has no tokens) and blocks.
 struct PackedSpan {
   int keys[2], blocks[2], n;
@@ -103,6 +144,11 @@ __device__ __forceinline__ bool packed_ragged(const PackedItem& it, int n) {
   return 128 * n > it.len && (it.len & 15) != 0;
 }
 
+__device__ __forceinline__ PackedItem uniform_item(const PackedItem& it) {
+  return PackedItem{__shfl_sync(0xffffffffu, it.row0, 0), __shfl_sync(0xffffffffu, it.len, 0),
+                    __shfl_sync(0xffffffffu, it.t0, 0), __shfl_sync(0xffffffffu, it.kvh, 0)};
+}
+
 template <int D>
 __global__ void __launch_bounds__(kPackedThreads, 1)
     packed_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -116,7 +162,8 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + Ly::oMisc + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const WaitCtl ctl{abort_flag, a.status, kWaitTimeoutNs};
-  const int i0 = __ldg(a.first + blockIdx.x), i1 = __ldg(a.first + blockIdx.x + 1);
+  const int i0 = __shfl_sync(0xffffffffu, __ldg(a.first + blockIdx.x), 0);
+  const int i1 = __shfl_sync(0xffffffffu, __ldg(a.first + blockIdx.x + 1), 0);
   auto item_at = [&](int i) -> PackedItem {
     const int4 v = __ldg(reinterpret_cast<const int4*>(a.items) + i);
     return PackedItem{v.x, v.y, v.z, v.w};
@@ -196,76 +243,101 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
     }
     __syncwarp();
   } else if (warp == 9) {
-    // ============================================================ issuer (one thread)
-    if (lane == 0) {
+    // ============================================================ issuer (one elected thread)
+    // The whole warp walks the items with values made uniform by a shuffle, and only the products and commits
+    // are the elected thread's: their descriptors then live in uniform registers.  With the walk itself inside
+    // `lane == 0` every product took about 130 cycles to issue, twice what it takes to run.
+    {
       uint32_t c = 0, qn[2] = {0, 0}, pn[2] = {0, 0};
       bool ok = true;
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint32_t q_desc = __shfl_sync(0xffffffffu, umma_desc_lo(smem_u32(sm + Ly::oQ)), 0);
+      const uint32_t kv_desc = __shfl_sync(0xffffffffu, umma_desc_lo(smem_u32(sm + Ly::oKV)), 0);
+      auto wait = [&](int bar, uint32_t parity, int site) {
+        return __shfl_sync(0xffffffffu, static_cast<int>(mbar_wait(&bars[bar], parity, ctl, site)), 0) != 0;
+      };
       auto issue_s = [&](int x, int j, int blocks, int keys, uint32_t kst) {
         const int cols = min(128, (keys - 128 * j + 15) & ~15);
         const uint32_t idesc = umma_idesc_bf16(128, cols, 0, 0);
-        const uint64_t ad = umma_desc_sw128(smem_u32(sm + Ly::oQ + x * Ly::kTileBytes), 16, 1024);
-        const uint64_t bd = umma_desc_sw128(smem_u32(sm + Ly::oKV + kst * Ly::kTileBytes), 16, 1024);
+        const uint32_t ad = q_desc + x * (Ly::kTileBytes >> 4), bd = kv_desc + kst * (Ly::kTileBytes >> 4);
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint64_t off = static_cast<uint64_t>(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
-          umma_ss(tmem + kPackedS + x * 128, ad + off, bd + off, idesc, kk > 0 ? 1u : 0u);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+            umma_ss(tm + kPackedS + x * 128, umma_desc(ad + off, 16), umma_desc(bd + off, 16), idesc, kk > 0 ? 1u : 0u);
+          }
+          umma_commit(&bars[Ly::bSFull + x]);
+          if (j == blocks - 1) umma_commit(&bars[Ly::bQEmpty + x]);
         }
-        umma_commit(&bars[Ly::bSFull + x]);
-        if (j == blocks - 1) umma_commit(&bars[Ly::bQEmpty + x]);
+        __syncwarp();
       };
-      auto issue_o = [&](int x, int j, int keys, uint32_t vst) {
+      auto issue_o = [&](int x, int j, int blocks, int keys, uint32_t vst, bool last_use) {
         constexpr uint32_t kIdesc = umma_idesc_bf16(128, D, 0, 1);
         const int steps = min(8, (keys - 128 * j + 15) >> 4);
-        const uint64_t bd = umma_desc_sw128(smem_u32(sm + Ly::oKV + vst * Ly::kTileBytes), 16384, 1024);
-        for (int kk = 0; kk < steps; ++kk)
-          umma_ts(tmem + kPackedO + x * 128, tmem + kPackedS + x * 128 + kk * 8, bd + static_cast<uint64_t>(kk * 128),
-                  kIdesc, (j > 0 || kk > 0) ? 1u : 0u);
+        const uint32_t bd = kv_desc + vst * (Ly::kTileBytes >> 4);
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            if (kk >= steps) break;
+            umma_ts(tm + kPackedO + x * 128, tm + kPackedS + x * 128 + kk * 8, umma_desc(bd + kk * 128, 16384), kIdesc,
+                    (j > 0 || kk > 0) ? 1u : 0u);
+          }
+          if (j == blocks - 1) umma_commit(&bars[Ly::bOFull + x]);
+          if (last_use) umma_commit(&bars[Ly::bEmpty + vst]);
+        }
+        __syncwarp();
       };
       for (int i = i0; i < i1 && ok; ++i) {
-        const PackedItem it = item_at(i);
+        const PackedItem it = uniform_item(item_at(i));
         const PackedSpan sp = packed_span(it, a);
-        uint32_t st = c % kStages;
-        ok = mbar_wait(&bars[Ly::bFull + st], (c / kStages) & 1, ctl, 211);
-        for (int x = 0; x < 2 && ok; ++x) {
-          if (sp.blocks[x] == 0) continue;
-          ok = mbar_wait(&bars[Ly::bQFull + x], qn[x] & 1, ctl, 212);
+        const uint32_t st = c % kStages;
+        ok = wait(Ly::bFull + st, (c / kStages) & 1, 211);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (!ok || sp.blocks[x] == 0) continue;
+          ok = wait(Ly::bQFull + x, qn[x] & 1, 212);
           ++qn[x];
-          if (!ok) break;
+          if (!ok) continue;
           tc_fence_after();
           issue_s(x, 0, sp.blocks[x], sp.keys[x], st);
         }
         if (!ok) break;
-        umma_commit(&bars[Ly::bEmpty + st]);
+        if (elect_one()) umma_commit(&bars[Ly::bEmpty + st]);
+        __syncwarp();
         ++c;
         for (int j = 0; j < sp.n && ok; ++j) {
           const uint32_t vst = c % kStages, kst = (c + 1) % kStages;
           const bool more = j + 1 < sp.n;
-          ok = mbar_wait(&bars[Ly::bFull + vst], (c / kStages) & 1, ctl, 213);
+          ok = wait(Ly::bFull + vst, (c / kStages) & 1, 213);
           bool k_here = false;
-          for (int x = 0; x < 2 && ok; ++x) {
-            if (j >= sp.blocks[x]) continue;
-            ok = mbar_wait(&bars[Ly::bPFull + x], pn[x] & 1, ctl, 214);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (!ok || j >= sp.blocks[x]) continue;
+            ok = wait(Ly::bPFull + x, pn[x] & 1, 214);
             ++pn[x];
-            if (!ok) break;
+            if (!ok) continue;
             tc_fence_after();
-            issue_o(x, j, sp.keys[x], vst);
-            if (j == sp.blocks[x] - 1) umma_commit(&bars[Ly::bOFull + x]);
-            if (x == 1 || j >= sp.blocks[1]) umma_commit(&bars[Ly::bEmpty + vst]);
+            issue_o(x, j, sp.blocks[x], sp.keys[x], vst, x == 1 || j >= sp.blocks[1]);
             if (j + 1 < sp.blocks[x]) {
-              if (!k_here) ok = mbar_wait(&bars[Ly::bFull + kst], ((c + 1) / kStages) & 1, ctl, 215);
+              if (!k_here) ok = wait(Ly::bFull + kst, ((c + 1) / kStages) & 1, 215);
               k_here = true;
-              if (!ok) break;
+              if (!ok) continue;
               tc_fence_after();
               issue_s(x, j + 1, sp.blocks[x], sp.keys[x], kst);
             }
           }
           if (!ok) break;
-          if (more) umma_commit(&bars[Ly::bEmpty + kst]);
+          if (more) {
+            if (elect_one()) umma_commit(&bars[Ly::bEmpty + kst]);
+            __syncwarp();
+          }
           c += more ? 2 : 1;
         }
       }
-      umma_commit(&bars[Ly::bDone]);
-      mbar_wait_drain(&bars[Ly::bDone], 0, ctl, 216);
+      if (elect_one()) {
+        umma_commit(&bars[Ly::bDone]);
+        mbar_wait_drain(&bars[Ly::bDone], 0, ctl, 216);
+      }
     }
     __syncwarp();
   } else if (warp == 10) {
@@ -306,37 +378,41 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
       const bool live = tl < a.tile_tokens && tok < it.len;
       // the row sees keys [0, seen); rows that are not stored see all and never vote
       const int seen = !live ? 0x40000000 : a.causal ? tok + 1 : it.len;
-      float m = 0.0f, l0 = 0.0f, l1 = 0.0f;
+      float m = 0.0f, l[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) l[q] = 0.0f;
       for (int j = 0; j < blocks; ++j, ++sn) {
         const int cols = min(128, keys - 128 * j), lim = seen - 128 * j;
-        const bool masked = __any_sync(0xffffffffu, lim < ((cols + 31) & ~31));
+        const bool masked = __any_sync(0xffffffffu, lim < 128);
         mbar_wait(&bars[Ly::bSFull + x], sn & 1, ctl, 231);
         tc_fence_after();
-        float top = -INFINITY;
+        // the whole row of S in registers; columns past `cols` hold older scores, masked below
+        float s[128];
 #pragma unroll
-        for (int c0 = 0; c0 < 128; c0 += 32) {
-          if (c0 >= cols) break;
-          float s[32];
-          tmem_ld32(s_col + c0, s);
-          tmem_wait_ld();
-          if (masked) {
+        for (int c0 = 0; c0 < 128; c0 += 32) tmem_ld32(s_col + c0, s + c0);
+        tmem_wait_ld();
+        if (masked) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (c0 + e >= lim) s[e] = -INFINITY;
-          }
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) top = max3(top, s[e], s[e + 1]);
+          for (int e = 0; e < 128; ++e)
+            if (e >= lim) s[e] = -INFINITY;
         }
-        const float t = top * cl;
+        float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int e = 4; e < 128; e += 8) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (e + 2 * q + 1 < 128) mx[q] = max3(mx[q], s[e + 2 * q], s[e + 2 * q + 1]);
+        }
+        const float t = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cl;
         if (j == 0) {
           m = t;
         } else if (__any_sync(0xffffffffu, live && t > m + kPackedRescale)) {
           // S of this block was committed after the product of the previous one, so O is complete
           const float up = fmaxf(m, t), f = up == m ? 1.0f : ex2_approx(m - up);
           m = up;
-          l0 *= f;
-          l1 *= f;
 #pragma unroll
+          for (int q = 0; q < 8; ++q) l[q] *= f;
+#pragma unroll 1
           for (int c0 = 0; c0 < D; c0 += 16) {
             float o[16];
             tmem_ld16(o_col + c0, o);
@@ -350,23 +426,21 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
 #pragma unroll
         for (int c0 = 0; c0 < 128; c0 += 32) {
           if (c0 >= cols) break;
-          float s[32];
-          tmem_ld32(s_col + c0, s);
-          tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) fma2(s[e], s[e + 1], s[e], s[e + 1], cl, cl, nm, nm);
-          if (masked) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (c0 + e >= lim) s[e] = -INFINITY;
+          for (int e = c0; e < c0 + 32; e += 2) {
+            fma2(s[e], s[e + 1], s[e], s[e + 1], cl, cl, nm, nm);
+            if ((e & 7) >= 8 - 2 * kPolyPairs) {
+              ex2_poly2(s[e], s[e + 1]);
+            } else {
+              s[e] = ex2_approx(s[e]);
+              s[e + 1] = ex2_approx(s[e + 1]);
+            }
           }
 #pragma unroll
-          for (int e = 0; e < 32; ++e) s[e] = ex2_approx(s[e]);
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) add2(l0, l1, l0, l1, s[e], s[e + 1]);
+          for (int e = c0; e < c0 + 32; e += 2) add2(l[e & 7], l[(e & 7) + 1], l[e & 7], l[(e & 7) + 1], s[e], s[e + 1]);
           uint32_t p[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) p[e] = pack_bf16x2(s[2 * e], s[2 * e + 1]);
+          for (int e = 0; e < 16; ++e) p[e] = pack_bf16x2(s[c0 + 2 * e], s[c0 + 2 * e + 1]);
           // P of these keys goes where S of keys at or before them was
           tmem_st16(s_col + c0 / 2, reinterpret_cast<const float*>(p));
         }
@@ -377,7 +451,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
       mbar_wait(&bars[Ly::bOFull + x], on & 1, ctl, 232);
       ++on;
       tc_fence_after();
-      const float rl = 1.0f / (l0 + l1);
+      const float rl = 1.0f / (((l[0] + l[1]) + (l[2] + l[3])) + ((l[4] + l[5]) + (l[6] + l[7])));
       uint16_t* dst = a.out + (static_cast<int64_t>(it.row0) + tok) * a.out_ld +
                       static_cast<int64_t>(it.kvh * a.group + hl) * a.out_hd;
 #pragma unroll

@@ -1722,6 +1722,14 @@ vsa_status vsa_packed_plan(const vsa_packed_desc* d, void* stream, vsa_packed_pl
       delete p;
       return st;
     }
+    st = with_head_dim(p->D, [&](auto dc) -> vsa_status {
+      constexpr int D = decltype(dc)::value;
+      return allow_smem(vsa::packed_attn_kernel<D>, vsa::PackedLayout<D>::bytes());
+    });
+    if (st != VSA_OK) {
+      delete p;
+      return st;
+    }
     const size_t item_bytes = align256(p->items.size() * sizeof(vsa::PackedItem));
     const size_t first_bytes = align256(p->first.size() * sizeof(int32_t));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1806,12 +1814,10 @@ vsa_status vsa_packed_attn(vsa_packed_plan_t p, const vsa_packed_args* a, void* 
     k.scale_log2 = static_cast<float>(static_cast<double>(p->dims.softmax_scale) * 1.4426950408889634);
     return with_head_dim(p->D, [&](auto dc) -> vsa_status {
       constexpr int D = decltype(dc)::value;
-      const size_t smem = vsa::PackedLayout<D>::bytes();
-      VSA_TRY(allow_smem(vsa::packed_attn_kernel<D>, smem));
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(static_cast<unsigned>(p->dims.ctas));
       cfg.blockDim = dim3(vsa::kPackedThreads);
-      cfg.dynamicSmemBytes = smem;
+      cfg.dynamicSmemBytes = vsa::PackedLayout<D>::bytes();  // allowed when the plan was made
       cfg.stream = static_cast<cudaStream_t>(stream);
       VSA_CUDA_TRY(cudaLaunchKernelEx(&cfg, vsa::packed_attn_kernel<D>, mq, mk, mv, k));
       return VSA_OK;
