@@ -1560,13 +1560,13 @@ namespace {
 
 constexpr int64_t kMaxPackedItems = int64_t(1) << 24;
 
-// Sizes and, with items not NULL, the schedule: every (sequence, pair of tiles, key head) is an item whose
-// cost is the key blocks its tiles visit plus kItemCost for what an item costs by itself (its query loads,
-// first scores and epilogue, about two blocks' time); items go longest first to the CTA with the least work
-// so far, so the CTAs finish within about one short item of each other.
+// Sizes and, with items not NULL, the schedule: every (sequence, 128 query rows, key head) is an item whose cost
+// is the key blocks it visits plus kItemCost for what an item costs by itself (its epilogue and the turn to
+// the next, about one block's time); items go longest first to the CTA with the least work so far, so the
+// CTAs finish within about one short item of each other.
 vsa_status packed_schedule(const vsa_packed_desc* d, int sms, vsa_packed_dims* dims, std::vector<vsa::PackedItem>* items,
                            std::vector<int32_t>* first) {
-  constexpr int64_t kItemCost = 2;
+  constexpr int64_t kItemCost = 1;
   if (d == nullptr) return fail(VSA_ERR_INVALID_ARG, "desc is NULL");
   if (d->n_seqs < 0) return fail(VSA_ERR_INVALID_ARG, "n_seqs < 0");
   if (d->n_seqs > 0 && d->lengths == nullptr) return fail(VSA_ERR_INVALID_ARG, "lengths is NULL");
@@ -1592,7 +1592,7 @@ vsa_status packed_schedule(const vsa_packed_desc* d, int sms, vsa_packed_dims* d
     if (n < 0) return fail(VSA_ERR_INVALID_ARG, "lengths[" + std::to_string(s) + "] is negative");
     dims->tokens += n;
     dims->pairs += d->causal ? n * (n + 1) / 2 : n * n;
-    dims->items += (n + 2 * tb - 1) / (2 * tb) * d->kv_heads;
+    dims->items += (n + tb - 1) / tb * d->kv_heads;
     if (dims->tokens >= (int64_t(1) << 31) - 1024)
       return fail(VSA_ERR_UNSUPPORTED, "the lengths' sum must stay below 2^31 - 1024");
   }
@@ -1609,10 +1609,8 @@ vsa_status packed_schedule(const vsa_packed_desc* d, int sms, vsa_packed_dims* d
   int64_t row0 = 0;
   for (int32_t s = 0; s < d->n_seqs; ++s) {
     const int64_t n = d->lengths[s];
-    for (int64_t t0 = 0; t0 < n; t0 += 2 * tb) {
-      int64_t cost = kItemCost;
-      for (int64_t t = t0; t < std::min(n, t0 + 2 * tb); t += tb)
-        cost += ((d->causal ? std::min(n, t + tb) : n) + 127) / 128;
+    for (int64_t t0 = 0; t0 < n; t0 += tb) {
+      const int64_t cost = kItemCost + ((d->causal ? std::min(n, t0 + tb) : n) + 127) / 128;
       for (int32_t h = 0; h < d->kv_heads; ++h)
         all.push_back({cost, vsa::PackedItem{static_cast<int32_t>(row0), static_cast<int32_t>(n), static_cast<int32_t>(t0), h}});
     }

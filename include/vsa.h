@@ -536,9 +536,9 @@ typedef struct vsa_packed_plan_s* vsa_packed_plan_t;
 typedef struct vsa_packed_dims {
   int64_t tokens;        /* sum of the lengths */
   int64_t pairs;         /* (query, key) pairs per query head */
-  int64_t items;         /* work items: up to two tiles of 128 query rows of one key head */
+  int64_t items;         /* work items: up to 128 query rows of one key head */
   int32_t ctas;          /* persistent CTAs they are spread over */
-  int32_t tile_tokens;   /* tokens per tile: floor(128 / (heads / kv_heads)) */
+  int32_t tile_tokens;   /* tokens per item: floor(128 / (heads / kv_heads)) */
   float softmax_scale;   /* the scale actually used */
 } vsa_packed_dims;
 vsa_status vsa_packed_plan(const vsa_packed_desc* desc, void* stream, vsa_packed_plan_t* out);

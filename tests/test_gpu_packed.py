@@ -206,6 +206,11 @@ def test_packed_bad_keys_stay_where_they_are_seen(vsa):
     got = run(vsa, q, k2, v, lengths, True)
     assert torch.equal(got[:250], want[:250]) and torch.equal(got[:, 2:], want[:, 2:])
     assert got[250:, :2].isnan().all()
+    for at in range(248, 256):  # whichever pipe takes a key's exponential
+        k2 = k.clone()
+        k2[at, 1, 5] = float("nan")
+        got = run(vsa, q, k2, v, lengths, True)
+        assert got[at:, 2:].isnan().all() and torch.equal(got[:at], want[:at])
     q2 = q.clone()
     q2[100, 1, 3] = float("nan")  # a query row harms itself only
     got = run(vsa, q2, k, v, lengths, True)

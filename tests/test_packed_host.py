@@ -36,11 +36,11 @@ def test_struct_layout(vsa, tmp_path, cname, pyname):
     assert got == [ctypes.sizeof(cls)] + [getattr(cls, f).offset for f, _ in cls._fields_]
 
 
-def spans(item, tb, causal):
-    """Keys and key blocks of the item's two tiles, as the kernel derives them."""
+def span(item, tb, causal):
+    """Keys and key blocks of an item, as the kernel derives them."""
     _, n, t0, _ = (int(x) for x in item)
-    keys = [0 if t >= n else min(n, t + tb) if causal else n for t in (t0, t0 + tb)]
-    return keys, [-(-k // 128) for k in keys]
+    keys = min(n, t0 + tb) if causal else n
+    return keys, -(-keys // 128)
 
 
 def lengths_of(seed):
@@ -70,13 +70,11 @@ def test_schedule_covers_every_row_once(vsa, lengths, heads, kv_heads, causal, s
     for row0, n, t0, h in items:
         assert n > 0 and length_at[row0] == n
         assert 0 <= t0 < n and 0 <= h < kv_heads
-        seen[row0 + t0:row0 + min(n, t0 + 2 * tb), h] += 1
-        keys, blocks = spans((row0, n, t0, h), tb, causal)
-        assert keys[0] >= 1 and max(keys) <= n and 128 * (max(blocks) - 1) < n
-        # the tile's own tokens are among the keys it sees: its first block is never fully masked
-        assert all(k == 0 or k >= min(n, t0 + (x + 1) * tb) or not causal for x, k in enumerate(keys))
-        assert blocks[1] == 0 or blocks[1] >= blocks[0]
-        cost.append(2 + sum(blocks))
+        seen[row0 + t0:row0 + min(n, t0 + tb), h] += 1
+        keys, blocks = span((row0, n, t0, h), tb, causal)
+        assert 1 <= keys <= n and 128 * (blocks - 1) < n
+        assert keys >= min(n, t0 + tb)  # every token of the item sees itself
+        cost.append(1 + blocks)
     assert (seen == 1).all()
     cost = np.array(cost)
     for c in range(d["ctas"]):
@@ -85,22 +83,6 @@ def test_schedule_covers_every_row_once(vsa, lengths, heads, kv_heads, causal, s
     if len(items):
         loads = [cost[first[c]:first[c + 1]].sum() for c in range(d["ctas"])]
         assert max(loads) <= cost.sum() / d["ctas"] + cost.max()
-
-
-def test_ring_order(vsa):
-    """The producer's, the issuer's and the helper's ring positions agree: per item K0, V0, K1, V1, ..."""
-    for n in range(1, 6):
-        producer = ["K0"]
-        for j in range(n):
-            producer += [f"V{j}"] + ([f"K{j + 1}"] if j + 1 < n else [])
-        c, issuer = 1, {0: "K0"}
-        for j in range(n):
-            issuer[c] = f"V{j}"
-            if j + 1 < n:
-                issuer[c + 1] = f"K{j + 1}"
-            c += 2 if j + 1 < n else 1
-        assert [issuer[i] for i in range(2 * n)] == producer and c == 2 * n
-        assert producer[2 * n - 1] == f"V{n - 1}"  # the helper's position
 
 
 @pytest.mark.parametrize("kw,status", [
