@@ -615,7 +615,8 @@ def _launch_index(names, *tensors):
         if t is None:
             continue
         if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{names[tensors.index(t)]} must be a torch.Tensor")
+            name = next(n for n, x in zip(names, tensors) if x is t)
+            raise TypeError(f"{name} must be a torch.Tensor")
         i = t.get_device()
         if index is None:
             index = i

@@ -6,9 +6,11 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <new>
+#include <type_traits>
 
 #include "status.h"
 #include "vsa.h"
@@ -27,6 +29,9 @@ __device__ __forceinline__ void unpack8(const uint4& u, float* f) {
     f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
   }
 }
+
+__device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -57,6 +62,11 @@ __device__ __forceinline__ void load8(const void* row, int chunk, float* f) {
 // The row stays in registers between the sums and the output, so it is read once.
 // max|y| = rsqrt(..) max|t w|, so one reduction gives both the sum of squares and the scale, and the
 // codes are E4M3(t w (448 / max|t w|)): the row factor cancels.
+//
+// A row is kC chunks of eight elements for each of its threads: one warp's 32 threads for rows of up to 1024
+// elements, else a CTA's (a barrier instead of shuffles alone).  The grid is as large as fits the GPU and
+// walks the rows, so that the weights are read once into registers and the next row's loads are in flight
+// while this one is summed and written.
 // ---------------------------------------------------------------------------------------------
 struct NormArgs {
   const uint16_t* x;
@@ -66,134 +76,182 @@ struct NormArgs {
   void* residual_out;
   float* scale;
   int64_t x_ld, res_ld, out_ld, res_out_ld;
-  int width;
+  int rows, width;
   float eps;
 };
 
-constexpr int kNormThreads = 256;
-constexpr int kNormChunks = 8;  // 16384 / 8 / 256: eight-element chunks of a row each thread may hold
+enum : int { kNoRes = 0, kResBf16 = 1, kResF32 = 2 };
 
-template <bool kRes, bool kResF32, bool kWF32, bool kF8>
-__global__ void __launch_bounds__(kNormThreads) rms_norm_kernel(const NormArgs a) {
-  const int64_t row = blockIdx.x;
+template <int kRes, bool kF8, bool kWF32, int kC, bool kWarp>
+__global__ void __launch_bounds__(kWarp ? 256 : kC <= 2 ? 1024 : 512) rms_norm_kernel(const NormArgs a) {
+  constexpr int kResWords = kRes == kResF32 ? 2 : 1;  // 16-byte words of a residual chunk
   const int chunks = a.width >> 3;
-  const uint16_t* x = a.x + row * a.x_ld;
-  const uint8_t* res = static_cast<const uint8_t*>(a.residual) + row * a.res_ld * (kResF32 ? 4 : 2);
-  uint8_t* res_out = a.residual_out == nullptr
-                         ? nullptr
-                         : static_cast<uint8_t*>(a.residual_out) + row * a.res_out_ld * (kResF32 ? 4 : 2);
-  const auto weight = [&](int c, float* w) {
-    if (a.weight != nullptr) {
-      load8<kWF32>(a.weight, c, w);
-    } else {
+  const int lanes = kWarp ? 32 : blockDim.x, lane = kWarp ? threadIdx.x & 31 : threadIdx.x;
+  const int step = kWarp ? gridDim.x * (blockDim.x >> 5) : gridDim.x;
+  int row = kWarp ? blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
+
+  uint4 xr[kC], rr[kRes ? kC * kResWords : 1];
+  const auto load = [&](int64_t row) {
+    const uint4* x = reinterpret_cast<const uint4*>(a.x + row * a.x_ld);
+    const uint4* r = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.residual) + row * a.res_ld * (2 * kResWords));
 #pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] = 1.0f;
-    }
-  };
-  float t[kNormChunks][8];
-  float ss = 0.0f, top = 0.0f;
+    for (int u = 0; u < kC; ++u) {
+      const int c = lane + u * lanes;
+      xr[u] = make_uint4(0u, 0u, 0u, 0u);  // chunks past the row add nothing to its sums
+      if (c < chunks) xr[u] = x[c];
+      if constexpr (kRes != kNoRes) {
 #pragma unroll
-  for (int u = 0; u < kNormChunks; ++u) {
-    const int c = threadIdx.x + u * kNormThreads;
-    if (c >= chunks) break;
-    load8<false>(x, c, t[u]);
-    if constexpr (kRes) {
-      float r[8];
-      load8<kResF32>(res, c, r);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) t[u][e] += r[e];
-      if (res_out != nullptr) {
-        if constexpr (kResF32) {
-          float4* p = reinterpret_cast<float4*>(res_out) + 2 * c;
-          p[0] = make_float4(t[u][0], t[u][1], t[u][2], t[u][3]);
-          p[1] = make_float4(t[u][4], t[u][5], t[u][6], t[u][7]);
-        } else {
-          reinterpret_cast<uint4*>(res_out)[c] = pack8(t[u]);
+        for (int k = 0; k < kResWords; ++k) {
+          rr[u * kResWords + k] = make_uint4(0u, 0u, 0u, 0u);
+          if (c < chunks) rr[u * kResWords + k] = r[c * kResWords + k];
         }
       }
     }
+  };
+  if (row < a.rows) load(row);
+  // the weights as they are stored: packed bf16 is half the registers, and more CTAs hold more loads in flight
+  constexpr int kWWords = kWF32 ? 2 : 1;
+  uint4 wr[kC * kWWords];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(t[u][e], t[u][e], ss);
-    if constexpr (kF8) {
-      float w[8];
-      weight(c, w);
+  for (int u = 0; u < kC; ++u) {
+    const int c = lane + u * lanes;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(t[u][e] * w[e]));
+    for (int k = 0; k < kWWords; ++k) {
+      const uint32_t one = kWF32 ? 0x3f800000u : 0x3f803f80u;
+      wr[u * kWWords + k] = make_uint4(one, one, one, one);
+      if (a.weight != nullptr && c < chunks) wr[u * kWWords + k] = static_cast<const uint4*>(a.weight)[c * kWWords + k];
     }
   }
-  __shared__ float2 part[2][kNormThreads / 32];
-  const auto reduce = [&](float2* slot, float* sum, float* most) {
+  const auto weights = [&](int u, float* w) {
+    if constexpr (kWF32) {
+      const uint4 p = wr[2 * u], q = wr[2 * u + 1];
+      const uint32_t v[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = __uint_as_float(v[e]);
+    } else {
+      unpack8(wr[u], w);
+    }
+  };
+  __shared__ float2 part[2][32];
+  int slot = 0;
+  const auto reduce = [&](float* sum, float* most) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
       *sum += __shfl_xor_sync(0xffffffffu, *sum, off);
-      *most = fmaxf(*most, __shfl_xor_sync(0xffffffffu, *most, off));
+      if constexpr (kF8) *most = fmaxf(*most, __shfl_xor_sync(0xffffffffu, *most, off));
     }
-    if ((threadIdx.x & 31) == 0) slot[threadIdx.x >> 5] = make_float2(*sum, *most);
-    __syncthreads();
-    *sum = 0.0f;
+    if constexpr (!kWarp) {
+      // two slots in turn: a slot is written again only behind the barrier that follows its last reads
+      if ((threadIdx.x & 31) == 0) part[slot][threadIdx.x >> 5] = make_float2(*sum, *most);
+      __syncthreads();
+      // every warp adds up the warps' partial sums: lane i reads the i-th, if there is one
+      const float2 v = (threadIdx.x & 31) < (blockDim.x >> 5) ? part[slot][threadIdx.x & 31] : make_float2(0.0f, 0.0f);
+      *sum = v.x;
+      *most = v.y;
 #pragma unroll
-    for (int i = 0; i < kNormThreads / 32; ++i) {
-      *sum += slot[i].x;
-      *most = fmaxf(*most, slot[i].y);
+      for (int off = 16; off > 0; off >>= 1) {
+        *sum += __shfl_xor_sync(0xffffffffu, *sum, off);
+        if constexpr (kF8) *most = fmaxf(*most, __shfl_xor_sync(0xffffffffu, *most, off));
+      }
+      slot ^= 1;
     }
   };
-  reduce(part[0], &ss, &top);
   const float n = static_cast<float>(a.width);
-  float mean = ss / n + a.eps, unit = 1.0f;
-  if (isinf(ss) || mean < 1e-30f) {  // the squares left binary32's range: once more, of the row times 2^-70 or 2^70
-    unit = isinf(ss) ? 0x1p-70f : 0x1p70f;
-    ss = top = 0.0f;
+  for (; row < a.rows; row = a.rows - row > step ? row + step : a.rows) {  // (rows may be up to 2^31 - 1)
+    float t[kC][8];
+    float ss = 0.0f, top = 0.0f;
 #pragma unroll
-    for (int u = 0; u < kNormChunks; ++u) {
-      const int c = threadIdx.x + u * kNormThreads;
-      if (c >= chunks) break;
-      float w[8];
-      weight(c, w);
+    for (int u = 0; u < kC; ++u) {
+      unpack8(xr[u], t[u]);
+      if constexpr (kRes == kResBf16) {
+        float r[8];
+        unpack8(rr[u], r);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        t[u][e] *= unit;
-        ss = fmaf(t[u][e], t[u][e], ss);
-        top = fmaxf(top, fabsf(t[u][e] * w[e]));
+        for (int e = 0; e < 8; ++e) t[u][e] += r[e];
+      } else if constexpr (kRes == kResF32) {
+        const uint4 p = rr[2 * u], q = rr[2 * u + 1];
+        const uint32_t r[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) t[u][e] += __uint_as_float(r[e]);
       }
     }
-    reduce(part[1], &ss, &top);
-    mean = ss / n + a.eps * unit * unit;
-  }
-  const float rstd = 1.0f / sqrtf(mean);  // of the row as t holds it
-  if constexpr (kF8) {
-    // rows whose 448 / max would overflow are raised by 2^64 first (exactly)
-    const float up = top < 1e-30f ? 0x1p64f : 1.0f;
-    const float f = top > 0.0f ? 448.0f / (top * up) : 0.0f;
-    if (threadIdx.x == 0) a.scale[row] = top > 0.0f ? top * rstd / 448.0f : isnan(ss) ? ss : 0.0f;
-    uint8_t* out = static_cast<uint8_t*>(a.out) + row * a.out_ld;
+    if (a.rows - row > step) load(row + step);
+    if constexpr (kRes != kNoRes) {
+      if (a.residual_out != nullptr) {
+        uint4* ro = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.residual_out) +
+                                             static_cast<int64_t>(row) * a.res_out_ld * (2 * kResWords));
 #pragma unroll
-    for (int u = 0; u < kNormChunks; ++u) {
-      const int c = threadIdx.x + u * kNormThreads;
-      if (c >= chunks) break;
-      uint32_t code[2] = {0u, 0u};
-      float w[8];
-      weight(c, w);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) t[u][e] = t[u][e] * w[e] * up * f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t two =
-            __nv_cvt_float2_to_fp8x2(make_float2(t[u][2 * j], t[u][2 * j + 1]), __NV_SATFINITE, __NV_E4M3);
-        code[j >> 1] |= two << (16 * (j & 1));
+        for (int u = 0; u < kC; ++u) {
+          const int c = lane + u * lanes;
+          if (c >= chunks) continue;
+          if constexpr (kRes == kResF32) {
+            const float* f = t[u];
+            ro[2 * c] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+            ro[2 * c + 1] = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7]));
+          } else {
+            ro[c] = pack8(t[u]);
+          }
+        }
       }
-      reinterpret_cast<uint2*>(out)[c] = make_uint2(code[0], code[1]);
     }
-  } else {
-    uint16_t* out = static_cast<uint16_t*>(a.out) + row * a.out_ld;
+    const auto sums = [&]() {
 #pragma unroll
-    for (int u = 0; u < kNormChunks; ++u) {
-      const int c = threadIdx.x + u * kNormThreads;
-      if (c >= chunks) break;
-      float w[8];
-      weight(c, w);
+      for (int u = 0; u < kC; ++u) {
+        float w[8];
+        if constexpr (kF8) weights(u, w);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) t[u][e] = t[u][e] * rstd * w[e];
-      reinterpret_cast<uint4*>(out)[c] = pack8(t[u]);
+        for (int e = 0; e < 8; ++e) {
+          ss = fmaf(t[u][e], t[u][e], ss);
+          if constexpr (kF8) top = fmaxf(top, fabsf(t[u][e] * w[e]));
+        }
+      }
+      reduce(&ss, &top);
+    };
+    sums();
+    float mean = ss / n + a.eps;
+    if (isinf(ss) || mean < 1e-30f) {  // the squares left binary32's range: once more, of the row times 2^-70 or 2^70
+      const float unit = isinf(ss) ? 0x1p-70f : 0x1p70f;
+      ss = top = 0.0f;
+#pragma unroll
+      for (int u = 0; u < kC; ++u) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) t[u][e] *= unit;
+      }
+      sums();
+      mean = ss / n + a.eps * unit * unit;
+    }
+    const float rstd = rsqrtf(mean);  // of the row as t holds it (within 2 ulp)
+    if constexpr (kF8) {
+      // rows whose 448 / max would overflow are raised by 2^64 first (exactly)
+      const float up = top < 1e-30f ? 0x1p64f : 1.0f;
+      const float f = top > 0.0f ? 448.0f / (top * up) : 0.0f;
+      if (lane == 0) a.scale[row] = top > 0.0f ? top * rstd / 448.0f : isnan(ss) ? ss : 0.0f;
+      uint2* out = reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + row * a.out_ld);
+#pragma unroll
+      for (int u = 0; u < kC; ++u) {
+        const int c = lane + u * lanes;
+        uint32_t code[2] = {0u, 0u};
+        float w[8];
+        weights(u, w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float v0 = t[u][2 * j] * w[2 * j] * up * f, v1 = t[u][2 * j + 1] * w[2 * j + 1] * up * f;
+          const uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(v0, v1), __NV_SATFINITE, __NV_E4M3);
+          code[j >> 1] |= two << (16 * (j & 1));
+        }
+        if (c < chunks) out[c] = make_uint2(code[0], code[1]);
+      }
+    } else {
+      uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row * a.out_ld);
+#pragma unroll
+      for (int u = 0; u < kC; ++u) {
+        const int c = lane + u * lanes;
+        float w[8];
+        weights(u, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) t[u][e] = t[u][e] * rstd * w[e];
+        if (c < chunks) out[c] = pack8(t[u]);
+      }
     }
   }
 }
@@ -223,23 +281,50 @@ struct RopeArgs {
   int64_t tokens, pos_rows;
   int heads, kv_heads, n_axes;
   int groups;      // lane groups per token (each takes every groups-th head)
-  int tokens_cta;  // tokens per CTA
+  int tokens_cta;  // tokens at a time
+  int span;        // how often, per CTA
   float eps;
 };
 
 constexpr int kRopeThreads = 256;
+// Tokens a CTA takes one after another, their sines computed together (it waits for positions once), and CTAs per SM
+// to compile for.  Measured on 56 + 56 heads, 75,008 tokens, D = 128 / 14,208, D = 96: one token 870 / 168 us, four
+// 731 / 140; 80 registers and three CTAs 721 / 145, 48 and five 1,017 / 146; a second row in flight 813 / 153.  What
+// bounds it is issue (74% of the slots, DRAM at 67 to 90%).
+constexpr int kRopeSpan = 4, kRopeCtas = 4;
+
+// Lanes per head row, 16 elements each, and head rows side by side in a warp (D = 96: six lanes, five rows).
+template <int D>
+struct RopeShape {
+  static constexpr int kLanes = D / 16, kRows = 32 / kLanes;
+};
 
 template <int D, bool kInter, bool kPosF32>
-__global__ void __launch_bounds__(kRopeThreads) qk_rope_kernel(const RopeArgs a, const __grid_constant__ RopeTable tab) {
-  constexpr int kPairs = D / 2;
-  constexpr int kLanes = D == 64 ? 4 : 8;  // lanes per head row: 16 elements each (D = 96: six of eight)
-  extern __shared__ float2 cs[];  // [tokens_cta][kPairs] (cos, sin)
-  const int64_t token0 = static_cast<int64_t>(blockIdx.x) * a.tokens_cta;
-  for (int i = threadIdx.x; i < a.tokens_cta * kPairs; i += kRopeThreads) {
-    const int tl = i / kPairs, p = i - tl * kPairs;
-    const int64_t token = token0 + tl;
-    if (token >= a.tokens) break;
-    const int64_t at = (token % a.pos_rows) * a.n_axes + tab.axis[p];
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas) qk_rope_kernel(const RopeArgs a, const __grid_constant__ RopeTable tab) {
+  constexpr int kPairs = D / 2, kLanes = RopeShape<D>::kLanes, kRows = RopeShape<D>::kRows;
+  extern __shared__ float2 cs[];  // [span * tokens_cta][kPairs] (cos, sin)
+  const int tokens = a.span * a.tokens_cta;  // of this CTA, tokens_cta at a time
+  const int64_t token0 = static_cast<int64_t>(blockIdx.x) * tokens;
+  const int wl = threadIdx.x & 31, lane = wl % kLanes;
+  const int group = (threadIdx.x >> 5) * kRows + wl / kLanes;
+  const int tl = group / a.groups, g = group - tl * a.groups;
+  const bool mine = wl < kRows * kLanes && tl < a.tokens_cta;
+  const int all = a.heads + a.kv_heads;
+  uint4 lo, hi;  // this group's next head row, in flight
+  const auto load = [&](int64_t token, int h) {
+    lo = hi = make_uint4(0u, 0u, 0u, 0u);
+    if (!mine || h >= all || token >= a.tokens) return;
+    const uint16_t* src = h >= a.heads ? a.k + token * a.k_ld + (h - a.heads) * a.k_hd : a.q + token * a.q_ld + h * a.q_hd;
+    lo = reinterpret_cast<const uint4*>(src)[lane];
+    hi = reinterpret_cast<const uint4*>(src + D / 2)[lane];
+  };
+  load(token0 + tl, g);
+  // while it comes, the sines and cosines of all the CTA's tokens
+  for (int i = threadIdx.x; i < tokens * kPairs; i += blockDim.x) {
+    const int t = i / kPairs, p = i - t * kPairs;
+    if (token0 + t >= a.tokens) break;
+    const int64_t row = a.pos_rows == a.tokens ? token0 + t : (token0 + t) % a.pos_rows;
+    const int64_t at = row * a.n_axes + tab.axis[p];
     const double pos = kPosF32 ? static_cast<double>(static_cast<const float*>(a.positions)[at])
                                : static_cast<double>(static_cast<const int32_t*>(a.positions)[at]);
     const double turn = pos * tab.turns[p];
@@ -248,58 +333,94 @@ __global__ void __launch_bounds__(kRopeThreads) qk_rope_kernel(const RopeArgs a,
     cs[i] = make_float2(c, s);
   }
   __syncthreads();
-  const int group = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
-  const int tl = group / a.groups, g = group - tl * a.groups;
-  const int64_t token = token0 + tl;
-  const bool live = tl < a.tokens_cta && token < a.tokens && lane < D / 16;
-  float co[8], si[8];
+  // the sum over the lanes of a head row
+  const auto row_sum = [&](float v) {
+    if constexpr (kLanes == 6) {
+      const int first = wl - lane;
+      v += __shfl_sync(0xffffffffu, v, first + (lane + 3) % 6);
+      const float u = __shfl_sync(0xffffffffu, v, first + (lane + 1) % 6);
+      return (v + u) + __shfl_sync(0xffffffffu, v, first + (lane + 2) % 6);
+    } else {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int p = kInter ? (e < 4 ? 4 * lane + e : kPairs / 2 + 4 * lane + e - 4) : 8 * lane + e;
-    const float2 v = live ? cs[tl * kPairs + p] : make_float2(1.0f, 0.0f);
-    co[e] = v.x;
-    si[e] = v.y;
-  }
-  const int all = a.heads + a.kv_heads;
-  for (int h0 = 0; h0 < all; h0 += a.groups) {
-    const int h = h0 + g;
-    const bool on = live && h < all;
-    const bool is_k = h >= a.heads;
-    const uint16_t* src = is_k ? a.k + token * a.k_ld + (h - a.heads) * a.k_hd : a.q + token * a.q_ld + h * a.q_hd;
-    const uint16_t* wt = is_k ? a.k_weight : a.q_weight;
-    float x[16];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) x[e] = 0.0f;
-    if (on) {
-      load8<false>(src, lane, x);
-      load8<false>(src + D / 2, lane, x + 8);
+      for (int off = kLanes / 2; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+      return v;
     }
-    float ss = 0.0f;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-    for (int off = kLanes / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-    if (on) {
-      if (wt != nullptr) {
-        const float rstd = 1.0f / sqrtf(ss / static_cast<float>(D) + a.eps);
-        float w[16];
-        load8<false>(wt, lane, w);
-        load8<false>(wt + D / 2, lane, w + 8);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] *= rstd * w[e];
-      }
-      float y[16];
+  };
+  const int rounds = (all + a.groups - 1) / a.groups;
+  float co[8], si[8];
+  for (int i = 0, s = 0, round = 0; i < a.span * rounds; ++i) {
+    const int64_t token = token0 + s * a.tokens_cta + tl;
+    const int h = round * a.groups + g;
+    const bool on = mine && token < a.tokens && h < all, is_k = h >= a.heads;
+    if (round == 0) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int ia = kInter ? (e < 4 ? 2 * e : 8 + 2 * (e - 4)) : e;
-        const int ib = kInter ? ia + 1 : e + 8;
-        y[ia] = x[ia] * co[e] - x[ib] * si[e];
-        y[ib] = x[ia] * si[e] + x[ib] * co[e];
+        const int p = kInter ? (e < 4 ? 4 * lane + e : kPairs / 2 + 4 * lane + e - 4) : 8 * lane + e;
+        const float2 v = on ? cs[(s * a.tokens_cta + tl) * kPairs + p] : make_float2(1.0f, 0.0f);
+        co[e] = v.x;
+        si[e] = v.y;
+      }
+    }
+    const uint32_t raw[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    if (++round == rounds) {
+      round = 0;
+      ++s;
+    }
+    if (i + 1 < a.span * rounds) load(token0 + s * a.tokens_cta + tl, round * a.groups + g);
+    // the row's factors: y = (x unit) rstd w (packed weights, unpacked where they are used: 64 registers a thread)
+    float unit = 1.0f, rstd = 1.0f;
+    uint32_t wt[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) wt[j] = 0x3f803f80u;
+    if (a.q_weight != nullptr || a.k_weight != nullptr) {
+      const uint16_t* weight = is_k ? a.k_weight : a.q_weight;
+      const auto mean_square = [&]() {
+        float ss = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float x0 = low(raw[j]) * unit, x1 = high(raw[j]) * unit;
+          ss = fmaf(x0, x0, ss);
+          ss = fmaf(x1, x1, ss);
+        }
+        return row_sum(ss) * (1.0f / static_cast<float>(D));
+      };
+      float mean = mean_square();
+      const bool far = weight != nullptr && (isinf(mean) || mean + a.eps < 1e-30f);
+      if (__any_sync(0xffffffffu, far)) {  // squares outside binary32's range: once more, of the row times 2^-70 or 2^70
+        if (far) unit = isinf(mean) ? 0x1p-70f : 0x1p70f;
+        mean = mean_square();
+      }
+      if (weight != nullptr && on) {
+        rstd = rsqrtf(mean + a.eps * unit * unit);
+        const uint4 w0 = reinterpret_cast<const uint4*>(weight)[lane], w1 = reinterpret_cast<const uint4*>(weight + D / 2)[lane];
+        wt[0] = w0.x; wt[1] = w0.y; wt[2] = w0.z; wt[3] = w0.w;
+        wt[4] = w1.x; wt[5] = w1.y; wt[6] = w1.z; wt[7] = w1.w;
+      } else {
+        unit = 1.0f;
+      }
+    }
+    if (on) {
+      uint32_t out[8];
+      const auto value = [&](float x, float w) { return x * unit * rstd * w; };
+      if constexpr (kInter) {  // a word holds a pair
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float x0 = value(low(raw[j]), low(wt[j])), x1 = value(high(raw[j]), high(wt[j]));
+          out[j] = pack2(x0 * co[j] - x1 * si[j], x0 * si[j] + x1 * co[j]);
+        }
+      } else {  // word j of the first half and of the second hold two
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float x0 = value(low(raw[j]), low(wt[j])), y0 = value(low(raw[j + 4]), low(wt[j + 4]));
+          const float x1 = value(high(raw[j]), high(wt[j])), y1 = value(high(raw[j + 4]), high(wt[j + 4]));
+          out[j] = pack2(x0 * co[2 * j] - y0 * si[2 * j], x1 * co[2 * j + 1] - y1 * si[2 * j + 1]);
+          out[j + 4] = pack2(x0 * si[2 * j] + y0 * co[2 * j], x1 * si[2 * j + 1] + y1 * co[2 * j + 1]);
+        }
       }
       uint16_t* dst =
           is_k ? a.k_out + token * a.ko_ld + (h - a.heads) * a.ko_hd : a.q_out + token * a.qo_ld + h * a.qo_hd;
-      reinterpret_cast<uint4*>(dst)[lane] = pack8(y);
-      reinterpret_cast<uint4*>(dst + D / 2)[lane] = pack8(y + 8);
+      reinterpret_cast<uint4*>(dst)[lane] = make_uint4(out[0], out[1], out[2], out[3]);
+      reinterpret_cast<uint4*>(dst + D / 2)[lane] = make_uint4(out[4], out[5], out[6], out[7]);
     }
   }
 }
@@ -315,6 +436,27 @@ vsa_status launch(const char* what, K kernel, unsigned grid, unsigned block, siz
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
   if (e != cudaSuccess) return set_error(VSA_ERR_CUDA, "%s launch: %s", what, cudaGetErrorString(e));
   return VSA_OK;
+}
+
+// As many CTAs as the GPU holds at once: a second wave of them would read its weights again and end unevenly
+// (a 4096-wide binary32 residual: 204 -> 270 us at half the CTAs, 272 at 3.5 of 4).
+template <int kRes, bool kF8, bool kWF32, bool kWarp>
+vsa_status launch_norm(const NormArgs& a, int per, int threads, int64_t groups, int sms, void* stream) {
+  static std::atomic<int> held[4][33];  // CTAs per SM, by chunks per thread and warps; 0: not asked yet
+  const auto kernel = per == 1   ? rms_norm_kernel<kRes, kF8, kWF32, 1, kWarp>
+                      : per == 2 ? rms_norm_kernel<kRes, kF8, kWF32, 2, kWarp>
+                      : per == 3 ? rms_norm_kernel<kRes, kF8, kWF32, 3, kWarp>
+                                 : rms_norm_kernel<kRes, kF8, kWF32, 4, kWarp>;
+  std::atomic<int>& h = held[per - 1][threads / 32];
+  int n = h.load(std::memory_order_relaxed);
+  if (n == 0) {
+    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0);
+    if (e != cudaSuccess) return set_error(VSA_ERR_CUDA, "rms_norm: %s", cudaGetErrorString(e));
+    n = std::max(1, n);
+    h.store(n, std::memory_order_relaxed);
+  }
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(groups, static_cast<int64_t>(sms) * n));
+  return launch("rms_norm", kernel, grid, static_cast<unsigned>(threads), 0, stream, a);
 }
 
 // A row stride in elements: a multiple of 8; an output's rows must not overlap.
@@ -395,23 +537,48 @@ vsa_status vsa_rms_norm(const vsa_rms_norm_args* p, void* stream) {
                       !p->residual_f32));
   VSA_TRY(check_alias("residual_out", p->residual, p->residual_stride, p->residual_out, p->residual_out_stride, p->rows,
                       true));
-  NormArgs a = {p->x,        p->residual,        p->weight,     p->out,
-                p->residual_out, p->scale,       p->x_stride,   p->residual_stride,
-                p->out_stride,   p->residual_out_stride, p->width, p->eps};
-  const auto go = [&](auto kernel) {
-    return launch("rms_norm", kernel, static_cast<unsigned>(p->rows), kNormThreads, 0, stream, a);
+  NormArgs a = {};
+  a.x = p->x;
+  a.residual = p->residual;
+  a.weight = p->weight;
+  a.out = p->out;
+  a.residual_out = p->residual_out;
+  a.scale = p->scale;
+  a.x_ld = p->x_stride;
+  a.res_ld = p->residual_stride;
+  a.out_ld = p->out_stride;
+  a.res_out_ld = p->residual_out_stride;
+  a.rows = static_cast<int>(p->rows);
+  a.width = p->width;
+  a.eps = p->eps;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return set_error(VSA_ERR_CUDA, "rms_norm: %s", cudaGetErrorString(e));
+  // Chunks per thread and threads per row: a warp up to 1024 elements; beyond, two to four chunks, about 256 threads
+  // with a residual and 512 without (half the registers and half the bytes a thread).  14,208 rows of 5376: with a
+  // residual 97.6 us (at 512 threads 95.8), without 57.9 (at 256 threads 60.8, at 672 of one chunk 95.7); 40,000
+  // rows of 2048: 52.5 us at two chunks, 61.6 at one.
+  const int chunks = p->width / 8;
+  const bool warp = chunks <= 128;
+  const int wide = res ? 256 : 512;
+  const int per = warp ? (chunks + 31) / 32 : std::min(4, std::max(2, (chunks + wide - 1) / wide));
+  const int threads = warp ? 256 : ((chunks + per - 1) / per + 31) / 32 * 32;
+  const int64_t groups = warp ? (p->rows + 7) / 8 : p->rows;
+  const auto go = [&](auto res_c) {
+    constexpr int R = decltype(res_c)::value;
+    const auto by_weight = [&](auto f8_c, auto wf_c) {
+      constexpr bool F = decltype(f8_c)::value, W = decltype(wf_c)::value;
+      return warp ? launch_norm<R, F, W, true>(a, per, threads, groups, sms, stream)
+                  : launch_norm<R, F, W, false>(a, per, threads, groups, sms, stream);
+    };
+    const std::true_type yes{};
+    const std::false_type no{};
+    if (p->out_e4m3) return p->weight_f32 ? by_weight(yes, yes) : by_weight(yes, no);
+    return p->weight_f32 ? by_weight(no, yes) : by_weight(no, no);
   };
-  const bool wf = p->weight_f32 != 0, f8 = p->out_e4m3 != 0;
-  if (!res) {
-    if (f8) return wf ? go(rms_norm_kernel<false, false, true, true>) : go(rms_norm_kernel<false, false, false, true>);
-    return wf ? go(rms_norm_kernel<false, false, true, false>) : go(rms_norm_kernel<false, false, false, false>);
-  }
-  if (p->residual_f32) {
-    if (f8) return wf ? go(rms_norm_kernel<true, true, true, true>) : go(rms_norm_kernel<true, true, false, true>);
-    return wf ? go(rms_norm_kernel<true, true, true, false>) : go(rms_norm_kernel<true, true, false, false>);
-  }
-  if (f8) return wf ? go(rms_norm_kernel<true, false, true, true>) : go(rms_norm_kernel<true, false, false, true>);
-  return wf ? go(rms_norm_kernel<true, false, true, false>) : go(rms_norm_kernel<true, false, false, false>);
+  if (!res) return go(std::integral_constant<int, kNoRes>{});
+  return p->residual_f32 ? go(std::integral_constant<int, kResF32>{}) : go(std::integral_constant<int, kResBf16>{});
 }
 
 vsa_status vsa_rope_create(const vsa_rope_desc* d, vsa_rope* out) {
@@ -537,14 +704,25 @@ vsa_status vsa_qk_rope(vsa_rope r, const vsa_qk_rope_args* p, void* stream) {
   a.kv_heads = p->kv_heads;
   a.n_axes = r->n_axes;
   a.eps = p->eps;
-  const int lanes = D == 64 ? 4 : 8, per_cta = kRopeThreads / lanes, all = p->heads + p->kv_heads;
+  // the heads of a token go over as many lane groups as share them evenly in the fewest rounds, several tokens to
+  // a CTA where one has few heads
+  const int rows = D == 64 ? RopeShape<64>::kRows : D == 96 ? RopeShape<96>::kRows : RopeShape<128>::kRows;
+  const int per_cta = kRopeThreads / 32 * rows, all = p->heads + p->kv_heads;
   const int rounds = (all + per_cta - 1) / per_cta;
   a.groups = (all + rounds - 1) / rounds;
   a.tokens_cta = std::max(1, per_cta / a.groups);
-  const int64_t grid = (p->tokens + a.tokens_cta - 1) / a.tokens_cta;
-  const size_t smem = static_cast<size_t>(a.tokens_cta) * (D / 2) * sizeof(float2);
+  const int threads = (a.groups * a.tokens_cta + rows - 1) / rows * 32;
+  // a CTA computes the sines of several tokens at once, since it waits for their positions; few tokens: one at a time
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return set_error(VSA_ERR_CUDA, "qk_rope: %s", cudaGetErrorString(e));
+  const int64_t turns = (p->tokens + a.tokens_cta - 1) / a.tokens_cta;
+  a.span = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kRopeSpan, turns / (8 * sms))));
+  const int64_t grid = (turns + a.span - 1) / a.span;
+  const size_t smem = static_cast<size_t>(a.span) * a.tokens_cta * (D / 2) * sizeof(float2);
   const auto go = [&](auto kernel) {
-    return launch("qk_rope", kernel, static_cast<unsigned>(grid), kRopeThreads, smem, stream, a, r->table);
+    return launch("qk_rope", kernel, static_cast<unsigned>(grid), static_cast<unsigned>(threads), smem, stream, a, r->table);
   };
   const auto by_kind = [&](auto half_i, auto half_f, auto next_i, auto next_f) {
     if (r->interleaved) return p->positions_f32 ? go(next_f) : go(next_i);

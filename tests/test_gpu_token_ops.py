@@ -257,6 +257,19 @@ def test_rope_norm_on_one_side_only(vsa):
     assert torch.equal(qo[..., still], q[..., still])
 
 
+def test_rope_norm_of_extreme_rows(vsa):
+    """Head rows whose squares leave binary32's range on either side, each its own row."""
+    g = gen(18)
+    scale = torch.tensor([1e-38, 1e-25, 1e-12, 1.0, 1e12, 1e19, 1e37, 0.0], device="cuda")
+    for D in (64, 96, 128):
+        q = (torch.randn(13, 8, D, generator=g, device="cuda").clamp(-4, 4) * scale[:, None]).to(BF16)
+        rope = vsa.vsa_rope_create(D, (D // 2,))
+        pos, w = positions_for(g, 13, 1), randn(g, D)
+        for eps in (1e-6, 1e-36):
+            qo, _ = vsa.vsa_qk_rope(rope, q, None, pos, q_weight=w, eps=eps)
+            check_rope(qo, rope, q, pos, w, eps)
+
+
 def test_rope_far_positions(vsa):
     """Positions up to the largest int32: the angle's error stays that of the 64-bit reference's own product
     (2^31 * 2^-53 = 2.4e-7 rad) plus binary32's."""
