@@ -60,6 +60,7 @@ struct PackedArgs {
 };
 
 constexpr int kPackedThreads = 352;
+constexpr int kAllKeys = 0x40000000;
 // Weights stay below 2^24, sums of fewer than 2^31 of them below 2^55; at 8 (a raise for every row whose logits
 // have a spread of 6 nats) the raises cost a third of the time on keys of uneven length.
 constexpr float kPackedRescale = 24.0f;
@@ -366,19 +367,19 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
     const int x = warp >> 2, r = threadIdx.x & 127;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t s_col = t_lane + x * 128, p_col = t_lane + kPackedP + x * 64, o_col = t_lane + kPackedO;
-    const int tl = r / a.group, hl = r - tl * a.group;  // token and head of the row inside an item
     const float cl = a.scale_log2;
     float* max_s = reinterpret_cast<float*>(sm + Ly::oMax);
     float2* sum_s = reinterpret_cast<float2*>(sm + Ly::oSum);
     uint32_t g = 0;  // blocks so far, of both groups
-    int n = 0;       // items so far
 
+    // (what little lives through the block loop is recomputed or packed: a row of scores leaves 40 registers)
     // item n - 1 is complete: this group's half of its O columns, over both groups' sums
-    uint32_t last_g = 0;  // its last block
-    bool pending = false;
-    auto epilogue = [&]() {
-      pending = false;
+    int pending = 0;  // 0: stored; 1 + parity of its last block
+    auto epilogue = [&](int n) {
+      const bool odd = pending == 2;
+      pending = 0;
       const PackedWork last = packed_work(a, i0 + n - 1);
+      const int tl = r / a.group, hl = r - tl * a.group;  // token and head of the row inside the item
       const int tok = last.t0 + tl;
       const bool live = tl < a.tile_tokens && tok < last.len;
       packed_wait(&bars[Ly::bSum], (n - 1) & 1, ctl, 232);
@@ -387,7 +388,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
       packed_wait(&bars[Ly::bOFull], (n - 1) & 1, ctl, 233);
       tc_fence_after();
       // O is relative to the maximum after the last block; a group without blocks has sum 0
-      const float m = (last_g & 1) ? s1.y : s0.y;
+      const float m = odd ? s1.y : s0.y;
       const float sum = (s0.x == 0.0f ? 0.0f : s0.x * ex2_approx(s0.y - m)) + (s1.x == 0.0f ? 0.0f : s1.x * ex2_approx(s1.y - m));
       const float rl = 1.0f / sum;
       uint16_t* dst = a.out + (static_cast<int64_t>(last.row0) + tok) * a.out_ld +
@@ -415,14 +416,12 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
 
     for (int i = i0; i < i1; ++i) {
       const PackedWork w = packed_work(a, i);
-      const int tok = w.t0 + tl;
-      const bool live = tl < a.tile_tokens && tok < w.len;
+      const int tl = r / a.group, tok = w.t0 + tl;
       // the row sees keys [0, seen); rows that are not stored see all and never vote
-      const int seen = !live ? 0x40000000 : a.causal ? tok + 1 : w.len;
+      const int seen = !(tl < a.tile_tokens && tok < w.len) ? kAllKeys : a.causal ? tok + 1 : w.len;
       float l[4], lm = 0.0f;  // this group's partial sums, relative to lm
 #pragma unroll
       for (int q = 0; q < 4; ++q) l[q] = 0.0f;
-      bool any = false;
       for (int j = 0; j < w.blocks; ++j, ++g) {
         if ((g & 1) != static_cast<uint32_t>(x)) continue;
         const uint32_t use = (g >> 1) & 1;  // parity of this use of the group's S and P buffers
@@ -462,9 +461,9 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
         const float m = (j == 0 || raise) ? t : before;
         max_s[(g & 1) * 128 + r] = m;
         mbar_arrive(&bars[Ly::bMax + (g & 1)]);
-        if (__any_sync(0xffffffffu, live && raise)) {
+        if (__any_sync(0xffffffffu, seen != kAllKeys && raise)) {
           // O must hold every block before this one, which may be waiting for this group's part of the last epilogue
-          if (pending) epilogue();
+          if (pending) epilogue(i - i0);
           packed_wait(&bars[Ly::bPEmpty + x], use ^ 1, ctl, 238);  // two blocks back, so that the next parity is the last block's
           packed_wait(&bars[Ly::bPEmpty + ((g - 1) & 1)], ((g - 1) >> 1) & 1, ctl, 236);
           tc_fence_after();
@@ -482,13 +481,12 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
         }
         tc_fence_before();
         mbar_arrive(&bars[Ly::bSEmpty + x]);  // the buffer is free for the group's next block
-        if (any && lm != m) {  // raised here, or by the other group since
+        if (j >= 2 && lm != m) {  // raised here, or by the other group since
           const float f = ex2_approx(lm - m);
 #pragma unroll
           for (int q = 0; q < 4; ++q) l[q] *= f;
         }
         lm = m;
-        any = true;
         // weights of 32 keys, their sum, and P, once the product two blocks back has read this buffer
         const float nm = m == -INFINITY ? 0.0f : -m;  // every score so far -inf: all weights zero
         auto keys32 = [&](int c0) {
@@ -514,21 +512,18 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
         if (cols > 32) keys32(32);
         if (cols > 64) keys32(64);
         if (cols > 96) keys32(96);
-        // the item before, whose last product has run meanwhile; this item's first overwrites O
-        if (pending) epilogue();
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&bars[Ly::bPFull + x]);
+        if (pending) epilogue(i - i0);  // the item before: its last product has run meanwhile, and this item's wait for it
       }
-      if (pending) epilogue();  // no block of this item was this group's
-      sum_s[(n & 1) * 256 + x * 128 + r] =
+      if (pending) epilogue(i - i0);  // no block of this item was this group's
+      sum_s[((i - i0) & 1) * 256 + x * 128 + r] =
           make_float2((l[0] + l[1]) + (l[2] + l[3]), lm);
       mbar_arrive(&bars[Ly::bSum]);
-      last_g = g - 1;
-      pending = true;
-      ++n;
+      pending = 1 + ((g - 1) & 1);
     }
-    if (pending) epilogue();
+    if (pending) epilogue(i1 - i0);
   }
 
   tc_fence_before();

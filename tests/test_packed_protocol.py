@@ -130,9 +130,9 @@ def replay(items, k_stages, v_stages, rng, raises):
                     yield ("PE", x), use ^ 1
                     assert P[x] is None
                     P[x] = g
+                    bars[("PF", x)].arrive()
                     if pending:
                         yield from epilogue()
-                    bars[("PF", x)].arrive()
                 g += 1
             if pending:
                 yield from epilogue()
