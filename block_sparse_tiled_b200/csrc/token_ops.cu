@@ -485,8 +485,8 @@ vsa_status check_ptr(const char* what, const void* p) {
 // In place means the same rows: an output that starts where an input starts has its strides.
 vsa_status check_alias(const char* what, const void* in, int64_t in_ld, const void* out, int64_t out_ld, int64_t rows,
                        bool same_type) {
-  if (in != out || in == nullptr || rows <= 1) return VSA_OK;
-  if (!same_type || in_ld != out_ld)
+  if (in != out || in == nullptr) return VSA_OK;
+  if (!same_type || (rows > 1 && in_ld != out_ld))
     return set_error(VSA_ERR_INVALID_ARG, "%s: an output in place of an input needs its type and stride", what);
   return VSA_OK;
 }
@@ -679,6 +679,7 @@ vsa_status vsa_qk_rope(vsa_rope r, const vsa_qk_rope_args* p, void* stream) {
   };
   VSA_TRY(check("q", p->heads, p->q, p->q_stride, p->q_head_stride, p->q_out, p->q_out_stride, p->q_out_head_stride,
                 p->q_weight));
+  if (p->kv_heads > 0 && p->k_out == p->q_out) return set_error(VSA_ERR_INVALID_ARG, "q_out and k_out are the same buffer");
   if (p->kv_heads > 0)
     VSA_TRY(check("k", p->kv_heads, p->k, p->k_stride, p->k_head_stride, p->k_out, p->k_out_stride,
                   p->k_out_head_stride, p->k_weight));
@@ -718,9 +719,10 @@ vsa_status vsa_qk_rope(vsa_rope r, const vsa_qk_rope_args* p, void* stream) {
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return set_error(VSA_ERR_CUDA, "qk_rope: %s", cudaGetErrorString(e));
   const int64_t turns = (p->tokens + a.tokens_cta - 1) / a.tokens_cta;
-  a.span = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kRopeSpan, turns / (8 * sms))));
+  const int64_t sines = static_cast<int64_t>(a.tokens_cta) * (D / 2) * sizeof(float2);  // at most 16 KB
+  a.span = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({kRopeSpan, turns / (8 * sms), (48 << 10) / sines})));
   const int64_t grid = (turns + a.span - 1) / a.span;
-  const size_t smem = static_cast<size_t>(a.span) * a.tokens_cta * (D / 2) * sizeof(float2);
+  const size_t smem = static_cast<size_t>(a.span * sines);
   const auto go = [&](auto kernel) {
     return launch("qk_rope", kernel, static_cast<unsigned>(grid), static_cast<unsigned>(threads), smem, stream, a, r->table);
   };

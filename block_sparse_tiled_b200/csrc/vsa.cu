@@ -1827,15 +1827,22 @@ vsa_status vsa_packed_attn(vsa_packed_plan_t p, const vsa_packed_args* a, void* 
 
 vsa_status vsa_packed_status(vsa_packed_plan_t p, void* stream, int32_t* code, int32_t* where) {
   if (p == nullptr) return vsa::set_error(VSA_ERR_INVALID_ARG, "plan is NULL");
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  int h[2] = {0, 0};
-  VSA_CUDA_TRY(cudaMemcpyAsync(h, p->d_status, sizeof h, cudaMemcpyDeviceToHost, s));
-  VSA_CUDA_TRY(cudaStreamSynchronize(s));
-  VSA_CUDA_TRY(cudaMemsetAsync(p->d_status, 0, sizeof h, s));
-  VSA_CUDA_TRY(cudaStreamSynchronize(s));
-  if (code) *code = h[0];
-  if (where) *where = h[1];
-  return VSA_OK;
+  try {
+    int dev = -1;
+    VSA_CUDA_TRY(cudaGetDevice(&dev));
+    if (dev != p->device) return fail(VSA_ERR_INVALID_ARG, "the current device is not the plan's device");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int h[2] = {0, 0};
+    VSA_CUDA_TRY(cudaMemcpyAsync(h, p->d_status, sizeof h, cudaMemcpyDeviceToHost, s));
+    VSA_CUDA_TRY(cudaStreamSynchronize(s));
+    VSA_CUDA_TRY(cudaMemsetAsync(p->d_status, 0, sizeof h, s));
+    VSA_CUDA_TRY(cudaStreamSynchronize(s));
+    if (code) *code = h[0];
+    if (where) *where = h[1];
+    return VSA_OK;
+  } catch (const std::exception&) {
+    return vsa::set_error(VSA_ERR_INVALID_ARG, "out of host memory");
+  }
 }
 
 }  // extern "C"

@@ -419,8 +419,9 @@ vsa_status vsa_plan_workspace(vsa_plan p, vsa_workspace_layout* out);
  *  - width: a multiple of 8 in [8, 16384]; any number of rows, 0 included.
  *  - strides: elements between rows, multiples of 8; an input's may be 0 (one
  *    row for all) or any, an output's at least the width.
- *  - In place: out may be x, residual_out may be residual or x (same type and
- *    stride); otherwise outputs must not overlap inputs or one another.
+ *  - In place: out may be x or residual, residual_out may be residual or x (of
+ *    the same type and stride); otherwise outputs must not overlap inputs or
+ *    one another.
  * No plan and no workspace: calls on different streams may overlap, and a call
  * may be captured.  The current device must be the one that holds the tensors.
  * Errors: VSA_ERR_INVALID_ARG, VSA_ERR_SHAPE, VSA_ERR_UNSUPPORTED, VSA_ERR_CUDA. */
@@ -516,7 +517,7 @@ vsa_status vsa_qk_rope(vsa_rope r, const vsa_qk_rope_args* args, void* stream);
  *  - q, out [tokens, heads, head_dim], k, v [tokens, kv_heads, head_dim] with
  *    any token and head strides that are multiples of 8 elements; tokens >=
  *    the lengths' sum.  Rows behind the last sequence are neither read nor
- *    written.
+ *    written.  out may be q (same strides); it must not overlap k or v.
  *  - A sequence's output depends on its own rows only, whatever the others
  *    hold.  Inside one, a masked key's score is replaced, so NaN or infinite
  *    keys stay where they are seen; a NaN or infinite value v[j] may also reach

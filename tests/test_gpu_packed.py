@@ -166,6 +166,17 @@ def test_packed_strides_and_rows_behind(vsa):
     check(vsa.vsa_packed_attn(plan, qh, ke, ve), qh, ke, ve, lengths, False)
 
 
+def test_packed_output_over_the_queries(vsa):
+    """out = q: every query row is read by one item only, before that item stores."""
+    lengths = (513, 40, 1, 300)
+    for heads, kv_heads, D in ((5, 1, 128), (4, 4, 64), (6, 2, 96)):
+        q, k, v = inputs(heads, sum(lengths), heads, kv_heads, D)
+        want = run(vsa, q, k, v, lengths, True)
+        plan = vsa.vsa_packed_plan(lengths, heads, kv_heads, D)
+        assert vsa.vsa_packed_attn(plan, q, k, v, out=q) is q
+        assert torch.equal(q, want)
+
+
 def test_packed_batch_of_equal_lengths(vsa):
     """[B, L, H, D] as B sequences of L."""
     q, k, v = inputs(8, 3 * 150, 4, 2, 64)

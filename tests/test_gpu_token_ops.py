@@ -257,6 +257,34 @@ def test_rope_norm_on_one_side_only(vsa):
     assert torch.equal(qo[..., still], q[..., still])
 
 
+@pytest.mark.parametrize("D", [64, 96, 128])
+def test_rope_many_tokens_of_one_head(vsa, D):
+    """One head, no keys: the most tokens a CTA takes at a time, over more tokens than the GPU holds CTAs for, so that
+    each takes several in turn; the last CTA's run past the end."""
+    g = gen(D)
+    T = 4 * 8 * 148 * 64 + 37
+    q = randn(g, T, 1, D)
+    rope = vsa.vsa_rope_create(D, (D // 4, D // 4))
+    pos = positions_for(g, T, 2)
+    w = randn(g, D)
+    buf = torch.full((T + 64, 1, D), 5.0, dtype=BF16, device="cuda")
+    out, _ = vsa.vsa_qk_rope(rope, q, None, pos, q_weight=w, q_out=buf[:T])
+    check_rope(out, rope, q, pos, w)
+    assert (buf[T:] == 5).all()
+
+
+def test_norm_many_rows(vsa):
+    """More rows than CTAs, uneven, at widths of every chunk count per thread and of the warp rows."""
+    g = gen(20)
+    for width in (200, 520, 1000, 1024, 1048, 2048, 4104, 5376, 8200, 12296):
+        rows = 5003 if width <= 5376 else 1301
+        x, w = randn(g, rows, width), randn(g, width)
+        check_norm(vsa.vsa_rms_norm(x, w, EPS), x, w, EPS)
+        r = randn(g, rows, width, dtype=F32)
+        check_norm(vsa.vsa_rms_norm(x, w, EPS, residual=r, out_dtype=E4M3), x, w, EPS, r)
+        check_norm(vsa.vsa_rms_norm(x, w, EPS, residual=x), x, w, EPS, x)
+
+
 def test_rope_norm_of_extreme_rows(vsa):
     """Head rows whose squares leave binary32's range on either side, each its own row."""
     g = gen(18)

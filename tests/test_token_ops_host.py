@@ -65,6 +65,10 @@ NORM = dict(rows=4, width=64, eps=1e-6, x=A, out=2 * A, x_stride=64, out_stride=
     (dict(out=A, out_e4m3=1, scale=4 * A), "VSA_ERR_INVALID_ARG"),  # codes over the bf16 rows
     (dict(residual=3 * A, residual_f32=1, residual_stride=64, residual_out=A, residual_out_stride=64),
      "VSA_ERR_INVALID_ARG"),
+    # a single row has no stride to compare, but types still differ: its writes would run ahead of its reads
+    (dict(rows=1, residual=3 * A, residual_f32=1, residual_stride=64, residual_out=A, residual_out_stride=64),
+     "VSA_ERR_INVALID_ARG"),
+    (dict(rows=1, out=A, out_e4m3=1, scale=4 * A), "VSA_ERR_INVALID_ARG"),
 ])
 def test_rms_norm_refusals(vsa, over, status):
     a = vsa.RmsNormArgs(**dict(NORM, **over))
@@ -142,6 +146,7 @@ K = dict(kv_heads=1, k=3 * A, k_out=4 * A, k_stride=64, k_head_stride=64, k_out_
     (dict(q_out=A, q_out_stride=256), "VSA_ERR_INVALID_ARG"),
     (dict(K, k_out=0), "VSA_ERR_INVALID_ARG"),
     (dict(K, k_stride=60), "VSA_ERR_INVALID_ARG"),
+    (dict(K, k_out=2 * A), "VSA_ERR_INVALID_ARG"),  # both outputs in one place
 ])
 def test_qk_rope_refusals(vsa, over, status):
     r = vsa.vsa_rope_create(64, (32,))
