@@ -30,6 +30,32 @@ __device__ __forceinline__ void unpack8(const uint4& u, float* f) {
   }
 }
 
+// Two elements per instruction, each rounded as by the scalar operation (the 8-bit norm of wide rows is bound by issue).
+__device__ __forceinline__ void fma2(float* d, float a0, float a1, float b0, float b1, float c0, float c1) {
+  asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(d[0]), "=f"(d[1])
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
+__device__ __forceinline__ void mul2(float* d, float a0, float a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(d[0]), "=f"(d[1])
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void add2(float* d, float a0, float a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(d[0]), "=f"(d[1])
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+// Largest of three; NaNs lose.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 __device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
@@ -66,7 +92,9 @@ __device__ __forceinline__ void load8(const void* row, int chunk, float* f) {
 // A row is kC chunks of eight elements for each of its threads: one warp's 32 threads for rows of up to 1024
 // elements, else a CTA's (a barrier instead of shuffles alone).  The grid is as large as fits the GPU and
 // walks the rows, so that the weights are read once into registers and the next row's loads are in flight
-// while this one is summed and written.
+// while this one is summed and written.  Bound by HBM where there are rows enough: 75,008 rows of 5376, bf16 residual,
+// 8-bit output 433 us = 6.52 TB/s; 14,208 rows without a residual 51 us = 6.0 TB/s; 1537 rows of 5120, binary32
+// residual 16.3 us = 5.3 TB/s; one row 2.6 us, the launch.
 // ---------------------------------------------------------------------------------------------
 struct NormArgs {
   const uint16_t* x;
@@ -82,8 +110,18 @@ struct NormArgs {
 
 enum : int { kNoRes = 0, kResBf16 = 1, kResF32 = 2 };
 
+// Threads of a row at most, by its chunks per thread, and the CTAs per SM to compile for.
+// Threads of a row at most, by its chunks per thread, and the CTAs per SM to compile for (more of them hold more loads
+// in flight, until the registers for them run out: 14,208 rows of 5376 without a residual at 3 chunks 58 us at two
+// CTAs, 51 at three, 55 at four; 30,000 bf16-residual rows of 4096 at 2 chunks 155 us at four, 137 at three; 75,008 rows
+// of 5376 with a residual at 3 chunks 433 us at two, 509 at three).
+template <int kC>
+constexpr int kNormThreads = kC == 4 ? 512 : 256;
+template <int kC, bool kRes>
+constexpr int kNormCtas = kC == 4 ? 1 : kC == 3 ? (kRes ? 2 : 3) : (kRes ? 3 : 4);
+
 template <int kRes, bool kF8, bool kWF32, int kC, bool kWarp>
-__global__ void __launch_bounds__(kWarp ? 256 : kC <= 2 ? 1024 : 512) rms_norm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(kWarp ? 256 : kNormThreads<kC>, kWarp ? 1 : kNormCtas<kC, kRes != kNoRes>) rms_norm_kernel(const NormArgs a) {
   constexpr int kResWords = kRes == kResF32 ? 2 : 1;  // 16-byte words of a residual chunk
   const int chunks = a.width >> 3;
   const int lanes = kWarp ? 32 : blockDim.x, lane = kWarp ? threadIdx.x & 31 : threadIdx.x;
@@ -132,27 +170,27 @@ __global__ void __launch_bounds__(kWarp ? 256 : kC <= 2 ? 1024 : 512) rms_norm_k
       unpack8(wr[u], w);
     }
   };
-  __shared__ float2 part[2][32];
+  constexpr int kWarps = kNormThreads<kC> / 32;  // of a row, at most
+  __shared__ float2 part[2][kWarps];
   int slot = 0;
+  const auto most_of = [](float v) {  // over the warp, of values >= 0 (their bits are in their order)
+    return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
+  };
   const auto reduce = [&](float* sum, float* most) {
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-      *sum += __shfl_xor_sync(0xffffffffu, *sum, off);
-      if constexpr (kF8) *most = fmaxf(*most, __shfl_xor_sync(0xffffffffu, *most, off));
-    }
+    for (int off = 16; off > 0; off >>= 1) *sum += __shfl_xor_sync(0xffffffffu, *sum, off);
+    if constexpr (kF8) *most = most_of(*most);
     if constexpr (!kWarp) {
       // two slots in turn: a slot is written again only behind the barrier that follows its last reads
       if ((threadIdx.x & 31) == 0) part[slot][threadIdx.x >> 5] = make_float2(*sum, *most);
       __syncthreads();
-      // every warp adds up the warps' partial sums: lane i reads the i-th, if there is one
-      const float2 v = (threadIdx.x & 31) < (blockDim.x >> 5) ? part[slot][threadIdx.x & 31] : make_float2(0.0f, 0.0f);
+      // every warp adds up the warps' partial sums: lane i reads the (i mod kWarps)-th, if there is one
+      const int i = threadIdx.x & (kWarps - 1);
+      const float2 v = i < (blockDim.x >> 5) ? part[slot][i] : make_float2(0.0f, 0.0f);
       *sum = v.x;
-      *most = v.y;
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) {
-        *sum += __shfl_xor_sync(0xffffffffu, *sum, off);
-        if constexpr (kF8) *most = fmaxf(*most, __shfl_xor_sync(0xffffffffu, *most, off));
-      }
+      for (int off = kWarps / 2; off > 0; off >>= 1) *sum += __shfl_xor_sync(0xffffffffu, *sum, off);
+      if constexpr (kF8) *most = most_of(v.y);
       slot ^= 1;
     }
   };
@@ -167,12 +205,13 @@ __global__ void __launch_bounds__(kWarp ? 256 : kC <= 2 ? 1024 : 512) rms_norm_k
         float r[8];
         unpack8(rr[u], r);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) t[u][e] += r[e];
+        for (int e = 0; e < 8; e += 2) add2(t[u] + e, t[u][e], t[u][e + 1], r[e], r[e + 1]);
       } else if constexpr (kRes == kResF32) {
         const uint4 p = rr[2 * u], q = rr[2 * u + 1];
         const uint32_t r[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) t[u][e] += __uint_as_float(r[e]);
+        for (int e = 0; e < 8; e += 2)
+          add2(t[u] + e, t[u][e], t[u][e + 1], __uint_as_float(r[e]), __uint_as_float(r[e + 1]));
       }
     }
     if (a.rows - row > step) load(row + step);
@@ -195,23 +234,29 @@ __global__ void __launch_bounds__(kWarp ? 256 : kC <= 2 ? 1024 : 512) rms_norm_k
       }
     }
     const auto sums = [&]() {
+      float s[2] = {0.0f, 0.0f};
 #pragma unroll
       for (int u = 0; u < kC; ++u) {
         float w[8];
         if constexpr (kF8) weights(u, w);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          ss = fmaf(t[u][e], t[u][e], ss);
-          if constexpr (kF8) top = fmaxf(top, fabsf(t[u][e] * w[e]));
+        for (int e = 0; e < 8; e += 2) {
+          fma2(s, t[u][e], t[u][e + 1], t[u][e], t[u][e + 1], s[0], s[1]);
+          if constexpr (kF8) {
+            float p[2];
+            mul2(p, t[u][e], t[u][e + 1], w[e], w[e + 1]);
+            top = max3(top, fabsf(p[0]), fabsf(p[1]));
+          }
         }
       }
+      ss = s[0] + s[1];
       reduce(&ss, &top);
     };
     sums();
     float mean = ss / n + a.eps;
     if (isinf(ss) || mean < 1e-30f) {  // the squares left binary32's range: once more, of the row times 2^-70 or 2^70
       const float unit = isinf(ss) ? 0x1p-70f : 0x1p70f;
-      ss = top = 0.0f;
+      top = 0.0f;
 #pragma unroll
       for (int u = 0; u < kC; ++u) {
 #pragma unroll
@@ -222,10 +267,18 @@ __global__ void __launch_bounds__(kWarp ? 256 : kC <= 2 ? 1024 : 512) rms_norm_k
     }
     const float rstd = rsqrtf(mean);  // of the row as t holds it (within 2 ulp)
     if constexpr (kF8) {
-      // rows whose 448 / max would overflow are raised by 2^64 first (exactly)
-      const float up = top < 1e-30f ? 0x1p64f : 1.0f;
-      const float f = top > 0.0f ? 448.0f / (top * up) : 0.0f;
       if (lane == 0) a.scale[row] = top > 0.0f ? top * rstd / 448.0f : isnan(ss) ? ss : 0.0f;
+      if (top < 1e-30f) {  // 448 / top may overflow: the row is raised by 2^64 (exactly)
+        top *= 0x1p64f;
+#pragma unroll
+        for (int u = 0; u < kC; ++u) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) t[u][e] *= 0x1p64f;
+        }
+      }
+      // 448 / top = f + rest
+      const float f = top > 0.0f ? 448.0f / top : 0.0f;
+      const float rest = f > 0.0f ? fmaf(-f, top, 448.0f) / top : 0.0f;
       uint2* out = reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + row * a.out_ld);
 #pragma unroll
       for (int u = 0; u < kC; ++u) {
@@ -235,8 +288,15 @@ __global__ void __launch_bounds__(kWarp ? 256 : kC <= 2 ? 1024 : 512) rms_norm_k
         weights(u, w);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float v0 = t[u][2 * j] * w[2 * j] * up * f, v1 = t[u][2 * j + 1] * w[2 * j + 1] * up * f;
-          const uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(v0, v1), __NV_SATFINITE, __NV_E4M3);
+          // t w (f + rest) with the product's remainder, rounded once: a code is off only where that rounding crosses a
+          // tie (1 or 2 codes of 7.9e6; 2 to 8 without the remainders)
+          const int i = 2 * j;
+          float p[2], q[2];
+          mul2(p, t[u][i], t[u][i + 1], w[i], w[i + 1]);
+          mul2(q, p[0], p[1], rest, rest);
+          fma2(q, fmaf(t[u][i], w[i], -p[0]), fmaf(t[u][i + 1], w[i + 1], -p[1]), f, f, q[0], q[1]);
+          fma2(q, p[0], p[1], f, f, q[0], q[1]);
+          const uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(q[0], q[1]), __NV_SATFINITE, __NV_E4M3);
           code[j >> 1] |= two << (16 * (j & 1));
         }
         if (c < chunks) out[c] = make_uint2(code[0], code[1]);
@@ -249,7 +309,10 @@ __global__ void __launch_bounds__(kWarp ? 256 : kC <= 2 ? 1024 : 512) rms_norm_k
         float w[8];
         weights(u, w);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) t[u][e] = t[u][e] * rstd * w[e];
+        for (int e = 0; e < 8; e += 2) {
+          mul2(t[u] + e, t[u][e], t[u][e + 1], rstd, rstd);
+          mul2(t[u] + e, t[u][e], t[u][e + 1], w[e], w[e + 1]);
+        }
         if (c < chunks) out[c] = pack8(t[u]);
       }
     }
@@ -443,7 +506,7 @@ vsa_status launch(const char* what, K kernel, unsigned grid, unsigned block, siz
 template <int kRes, bool kF8, bool kWF32, bool kWarp>
 vsa_status launch_norm(const NormArgs& a, int per, int threads, int64_t groups, int sms, void* stream) {
   static std::atomic<int> held[4][33];  // CTAs per SM, by chunks per thread and warps; 0: not asked yet
-  const auto kernel = per == 1   ? rms_norm_kernel<kRes, kF8, kWF32, 1, kWarp>
+  const auto kernel = kWarp && per == 1 ? rms_norm_kernel<kRes, kF8, kWF32, 1, true>
                       : per == 2 ? rms_norm_kernel<kRes, kF8, kWF32, 2, kWarp>
                       : per == 3 ? rms_norm_kernel<kRes, kF8, kWF32, 3, kWarp>
                                  : rms_norm_kernel<kRes, kF8, kWF32, 4, kWarp>;
@@ -555,13 +618,13 @@ vsa_status vsa_rms_norm(const vsa_rms_norm_args* p, void* stream) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return set_error(VSA_ERR_CUDA, "rms_norm: %s", cudaGetErrorString(e));
-  // Chunks per thread and threads per row: a warp up to 1024 elements; beyond, two to four chunks, about 256 threads
-  // with a residual and 512 without (half the registers and half the bytes a thread).  14,208 rows of 5376: with a
-  // residual 97.6 us (at 512 threads 95.8), without 57.9 (at 256 threads 60.8, at 672 of one chunk 95.7); 40,000
-  // rows of 2048: 52.5 us at two chunks, 61.6 at one.
+  // Chunks per thread and threads per row: a warp up to 1024 elements; beyond, two to four chunks, for about 256 threads
+  // (5376 elements without a residual: 51 us at 3 chunks, 58 at 2, 96 at one; 40,000 rows of 2048: 52.5 us at two
+  // chunks, 61.6 at one).  A binary32 residual of 385 to 512 chunks takes three (30,000 rows of 4096: 245 us, 260 at two;
+  // with 8-bit output 213, 243 at two).
   const int chunks = p->width / 8;
   const bool warp = chunks <= 128;
-  const int wide = res ? 256 : 512;
+  const int wide = res && p->residual_f32 && chunks <= 512 ? 192 : 256;
   const int per = warp ? (chunks + 31) / 32 : std::min(4, std::max(2, (chunks + wide - 1) / wide));
   const int threads = warp ? 256 : ((chunks + per - 1) / per + 31) / 32 * 32;
   const int64_t groups = warp ? (p->rows + 7) / 8 : p->rows;

@@ -69,6 +69,26 @@ def check_norm(got, x, weight, eps, residual=None):
     assert (out.double().abs().amax(-1)[~live] == 0.0).all()
 
 
+@pytest.mark.parametrize("residual", [None, BF16, F32])
+@pytest.mark.parametrize("rows,width", [(300, 1016), (1537, 5120), (700, 8200)])
+def test_norm_codes_are_the_nearest(vsa, rows, width, residual):
+    """A code is E4M3(448 y / max|y|), off only where that value lies within the binary32 roundings of a tie:
+    of t, of the largest product and its t, and of the value itself, 2^-24 of it each."""
+    g = gen(rows + width)
+    x, w = randn(g, rows, width), 1.0 + randn(g, width, scale=0.2)
+    r = None if residual is None else randn(g, rows, width, scale=3.0, dtype=residual)
+    out = torch.empty(rows, width, dtype=E4M3, device="cuda")
+    scale = torch.empty(rows, dtype=F32, device="cuda")
+    vsa.vsa_rms_norm(x, w, EPS, residual=r, out=out, scale=scale)
+    _, y = norm_ref(x, w, EPS, r)
+    value = 448.0 * y / y.abs().amax(-1, keepdim=True)
+    nearest = value.float().to(E4M3)
+    off = out.double() != nearest.double()
+    tie = (out.double() + nearest.double())[off] / 2
+    # (2^-25 more: the oracle's own rounding to binary32 before the conversion)
+    assert ((tie - value[off]).abs() <= 4.5 * 2.0 ** -24 * value[off].abs()).all()
+
+
 @pytest.mark.parametrize("out_dtype", [BF16, E4M3])
 @pytest.mark.parametrize("residual", [None, BF16, F32])
 @pytest.mark.parametrize("rows,width", [(1, 8), (3, 64), (5, 136), (33, 768), (257, 1032), (1, 5120), (64, 5376),
