@@ -351,9 +351,10 @@ struct RopeArgs {
 
 constexpr int kRopeThreads = 256;
 // Tokens a CTA takes one after another, their sines computed together (it waits for positions once), and CTAs per SM
-// to compile for.  Measured on 56 + 56 heads, 75,008 tokens, D = 128 / 14,208, D = 96: one token 870 / 168 us, four
-// 731 / 140; 80 registers and three CTAs 721 / 145, 48 and five 1,017 / 146; a second row in flight 813 / 153.  What
-// bounds it is issue (74% of the slots, DRAM at 67 to 90%).
+// to compile for.  Measured on 56 + 56 heads with the head norm, 75,008 tokens, D = 128, neighbouring pairs / 14,208
+// tokens, D = 96, halves: four tokens 729 us (5.9 TB/s) / 122 us (5.0 TB/s), two 743 / 127, eight 733 / 124; 80
+// registers and three CTAs 717 / 129.  With one element per instruction 737 / 139: issue bounds it (79% of the
+// slots then), HBM the long wide case.
 constexpr int kRopeSpan = 4, kRopeCtas = 4;
 
 // Lanes per head row, 16 elements each, and head rows side by side in a warp (D = 96: six lanes, five rows).
@@ -424,60 +425,72 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) qk_rope_kernel(const 
         si[e] = v.y;
       }
     }
-    const uint32_t raw[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    uint32_t raw[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
     if (++round == rounds) {
       round = 0;
       ++s;
     }
     if (i + 1 < a.span * rounds) load(token0 + s * a.tokens_cta + tl, round * a.groups + g);
-    // the row's factors: y = (x unit) rstd w (packed weights, unpacked where they are used: 64 registers a thread)
-    float unit = 1.0f, rstd = 1.0f;
+    // the row's factors: y = x rstd w (packed weights, unpacked where they are used: 64 registers a thread)
+    float rstd = 1.0f;
     uint32_t wt[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) wt[j] = 0x3f803f80u;
     if (a.q_weight != nullptr || a.k_weight != nullptr) {
       const uint16_t* weight = is_k ? a.k_weight : a.q_weight;
       const auto mean_square = [&]() {
-        float ss = 0.0f;
+        float ss[2] = {0.0f, 0.0f};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float x0 = low(raw[j]) * unit, x1 = high(raw[j]) * unit;
-          ss = fmaf(x0, x0, ss);
-          ss = fmaf(x1, x1, ss);
-        }
-        return row_sum(ss) * (1.0f / static_cast<float>(D));
+        for (int j = 0; j < 8; ++j) fma2(ss, low(raw[j]), high(raw[j]), low(raw[j]), high(raw[j]), ss[0], ss[1]);
+        return row_sum(ss[0] + ss[1]) * (1.0f / static_cast<float>(D));
       };
-      float mean = mean_square();
-      const bool far = weight != nullptr && (isinf(mean) || mean + a.eps < 1e-30f);
+      float mean = mean_square(), eps = a.eps;
+      const bool far = weight != nullptr && (isinf(mean) || mean + eps < 1e-30f);
       if (__any_sync(0xffffffffu, far)) {  // squares outside binary32's range: once more, of the row times 2^-70 or 2^70
-        if (far) unit = isinf(mean) ? 0x1p-70f : 0x1p70f;
+        const float unit = !far ? 1.0f : isinf(mean) ? 0x1p-70f : 0x1p70f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) raw[j] = pack2(low(raw[j]) * unit, high(raw[j]) * unit);
+        eps = eps * unit * unit;  // (unit squared leaves the range)
         mean = mean_square();
       }
       if (weight != nullptr && on) {
-        rstd = rsqrtf(mean + a.eps * unit * unit);
+        rstd = rsqrtf(mean + eps);
         const uint4 w0 = reinterpret_cast<const uint4*>(weight)[lane], w1 = reinterpret_cast<const uint4*>(weight + D / 2)[lane];
         wt[0] = w0.x; wt[1] = w0.y; wt[2] = w0.z; wt[3] = w0.w;
         wt[4] = w1.x; wt[5] = w1.y; wt[6] = w1.z; wt[7] = w1.w;
-      } else {
-        unit = 1.0f;
       }
     }
     if (on) {
       uint32_t out[8];
-      const auto value = [&](float x, float w) { return x * unit * rstd * w; };
+      // two pairs (x, y) at a time: x c - y s and x s + y c
+      const auto turn = [&](float* x, float* y, int p) {
+        float u[2], v[2];
+        mul2(u, y[0], y[1], si[p], si[p + 1]);
+        mul2(v, y[0], y[1], co[p], co[p + 1]);
+        fma2(y, x[0], x[1], si[p], si[p + 1], v[0], v[1]);
+        x[0] = fmaf(x[0], co[p], -u[0]);
+        x[1] = fmaf(x[1], co[p + 1], -u[1]);
+      };
+      const auto norm2 = [&](float* x, float w0, float w1) {
+        mul2(x, x[0], x[1], rstd, rstd);
+        mul2(x, x[0], x[1], w0, w1);
+      };
       if constexpr (kInter) {  // a word holds a pair
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float x0 = value(low(raw[j]), low(wt[j])), x1 = value(high(raw[j]), high(wt[j]));
-          out[j] = pack2(x0 * co[j] - x1 * si[j], x0 * si[j] + x1 * co[j]);
+          float x[2] = {low(raw[j]), high(raw[j])};
+          norm2(x, low(wt[j]), high(wt[j]));
+          out[j] = pack2(x[0] * co[j] - x[1] * si[j], x[0] * si[j] + x[1] * co[j]);
         }
       } else {  // word j of the first half and of the second hold two
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float x0 = value(low(raw[j]), low(wt[j])), y0 = value(low(raw[j + 4]), low(wt[j + 4]));
-          const float x1 = value(high(raw[j]), high(wt[j])), y1 = value(high(raw[j + 4]), high(wt[j + 4]));
-          out[j] = pack2(x0 * co[2 * j] - y0 * si[2 * j], x1 * co[2 * j + 1] - y1 * si[2 * j + 1]);
-          out[j + 4] = pack2(x0 * si[2 * j] + y0 * co[2 * j], x1 * si[2 * j + 1] + y1 * co[2 * j + 1]);
+          float x[2] = {low(raw[j]), high(raw[j])}, y[2] = {low(raw[j + 4]), high(raw[j + 4])};
+          norm2(x, low(wt[j]), high(wt[j]));
+          norm2(y, low(wt[j + 4]), high(wt[j + 4]));
+          turn(x, y, 2 * j);
+          out[j] = pack2(x[0], x[1]);
+          out[j + 4] = pack2(y[0], y[1]);
         }
       }
       uint16_t* dst =
