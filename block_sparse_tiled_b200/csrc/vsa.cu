@@ -1794,6 +1794,9 @@ vsa_status vsa_packed_attn(vsa_packed_plan_t p, const vsa_packed_args* a, void* 
     VSA_TRY(check_packed_strides("k", n, p->kv_heads, p->D, a->k_stride, a->k_head_stride, false));
     VSA_TRY(check_packed_strides("v", n, p->kv_heads, p->D, a->v_stride, a->v_head_stride, false));
     VSA_TRY(check_packed_strides("out", n, p->heads, p->D, a->out_stride, a->out_head_stride, true));
+    if (a->out == a->k || a->out == a->v) return fail(VSA_ERR_INVALID_ARG, "out must not overlap k or v");
+    if (a->out == a->q && (a->out_stride != a->q_stride || a->out_head_stride != a->q_head_stride))
+      return fail(VSA_ERR_INVALID_ARG, "out over q needs q's strides");
     const int g = p->heads / p->kv_heads, tb = p->dims.tile_tokens;
     CUtensorMap mq, mk, mv;
     VSA_TRY(make_packed_map(&mq, a->q, n, p->heads, p->D, a->q_stride, a->q_head_stride, g, tb));

@@ -284,3 +284,18 @@ def test_packed_binding_refusals(vsa):
     empty.destroy()
     with pytest.raises(ValueError):
         vsa.vsa_packed_attn(empty, q, k, v)
+
+
+def test_packed_refuses_an_output_over_its_inputs(vsa):
+    """The output may replace q in place, row for row; over k or v, or over q in another layout, items would
+    overwrite what others still read."""
+    q, k, v = inputs(12, 256, 2, 2, 64)
+    plan = vsa.vsa_packed_plan([200, 56], 2, 2, 64)
+    for other in (k, v):
+        with pytest.raises(vsa.VsaError):
+            vsa.vsa_packed_attn(plan, q, k, v, out=other)
+    turned = q.view(2, 256, 64).transpose(0, 1)  # q's memory, heads apart
+    with pytest.raises(vsa.VsaError):
+        vsa.vsa_packed_attn(plan, q, k, v, out=turned)
+    want = vsa.vsa_packed_attn(plan, q, k, v)
+    assert torch.equal(vsa.vsa_packed_attn(plan, q, k, v, out=q), want)
