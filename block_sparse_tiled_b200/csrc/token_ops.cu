@@ -341,7 +341,7 @@ struct RopeArgs {
   int64_t q_ld, q_hd, k_ld, k_hd, qo_ld, qo_hd, ko_ld, ko_hd;  // token and head strides, elements
   const uint16_t *q_weight, *k_weight;
   const void* positions;
-  int64_t tokens, pos_rows;
+  uint32_t tokens, pos_rows;
   int heads, kv_heads, n_axes;
   int groups;      // lane groups per token (each takes every groups-th head)
   int tokens_cta;  // tokens at a time
@@ -351,10 +351,10 @@ struct RopeArgs {
 
 constexpr int kRopeThreads = 256;
 // Tokens a CTA takes one after another, their sines computed together (it waits for positions once), and CTAs per SM
-// to compile for.  Measured on 56 + 56 heads with the head norm, 75,008 tokens, D = 128, neighbouring pairs / 14,208
-// tokens, D = 96, halves: four tokens 729 us (5.9 TB/s) / 122 us (5.0 TB/s), two 743 / 127, eight 733 / 124; 80
-// registers and three CTAs 717 / 129.  With one element per instruction 737 / 139: issue bounds it (79% of the
-// slots then), HBM the long wide case.
+// to compile for.  On 56 + 56 heads with the head norm, 75,008 tokens, D = 128, neighbouring pairs / 14,208 tokens,
+// D = 96, halves: 705 us (6.1 TB/s) / 117 us (5.2 TB/s).  Issue bounds it (78% of the slots at D = 96), HBM the long
+// wide case: with token numbers of 64 bits 729 / 122, with one element per instruction as well 737 / 139.  Measured at
+// 729 / 122: two tokens 743 / 127, eight 733 / 124; 80 registers and three CTAs 717 / 129.
 constexpr int kRopeSpan = 4, kRopeCtas = 4;
 
 // Lanes per head row, 16 elements each, and head rows side by side in a warp (D = 96: six lanes, five rows).
@@ -368,17 +368,20 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) qk_rope_kernel(const 
   constexpr int kPairs = D / 2, kLanes = RopeShape<D>::kLanes, kRows = RopeShape<D>::kRows;
   extern __shared__ float2 cs[];  // [span * tokens_cta][kPairs] (cos, sin)
   const int tokens = a.span * a.tokens_cta;  // of this CTA, tokens_cta at a time
-  const int64_t token0 = static_cast<int64_t>(blockIdx.x) * tokens;
+  const uint32_t token0 = blockIdx.x * static_cast<uint32_t>(tokens);  // tokens stay below 2^31
   const int wl = threadIdx.x & 31, lane = wl % kLanes;
   const int group = (threadIdx.x >> 5) * kRows + wl / kLanes;
   const int tl = group / a.groups, g = group - tl * a.groups;
   const bool mine = wl < kRows * kLanes && tl < a.tokens_cta;
-  const int all = a.heads + a.kv_heads;
+  const uint32_t all = a.heads + a.kv_heads, heads = a.heads;
+  const auto row_at = [](uint32_t token, int64_t ld, uint32_t head, int64_t hd) {
+    return static_cast<uint64_t>(token) * static_cast<uint64_t>(ld) + static_cast<uint64_t>(head) * static_cast<uint64_t>(hd);
+  };
   uint4 lo, hi;  // this group's next head row, in flight
-  const auto load = [&](int64_t token, int h) {
+  const auto load = [&](uint32_t token, uint32_t h) {
     lo = hi = make_uint4(0u, 0u, 0u, 0u);
     if (!mine || h >= all || token >= a.tokens) return;
-    const uint16_t* src = h >= a.heads ? a.k + token * a.k_ld + (h - a.heads) * a.k_hd : a.q + token * a.q_ld + h * a.q_hd;
+    const uint16_t* src = h >= heads ? a.k + row_at(token, a.k_ld, h - heads, a.k_hd) : a.q + row_at(token, a.q_ld, h, a.q_hd);
     lo = reinterpret_cast<const uint4*>(src)[lane];
     hi = reinterpret_cast<const uint4*>(src + D / 2)[lane];
   };
@@ -413,9 +416,9 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) qk_rope_kernel(const 
   const int rounds = (all + a.groups - 1) / a.groups;
   float co[8], si[8];
   for (int i = 0, s = 0, round = 0; i < a.span * rounds; ++i) {
-    const int64_t token = token0 + s * a.tokens_cta + tl;
-    const int h = round * a.groups + g;
-    const bool on = mine && token < a.tokens && h < all, is_k = h >= a.heads;
+    const uint32_t token = token0 + s * a.tokens_cta + tl;
+    const uint32_t h = round * a.groups + g;
+    const bool on = mine && token < a.tokens && h < all, is_k = h >= heads;
     if (round == 0) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -494,7 +497,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) qk_rope_kernel(const 
         }
       }
       uint16_t* dst =
-          is_k ? a.k_out + token * a.ko_ld + (h - a.heads) * a.ko_hd : a.q_out + token * a.qo_ld + h * a.qo_hd;
+          is_k ? a.k_out + row_at(token, a.ko_ld, h - heads, a.ko_hd) : a.q_out + row_at(token, a.qo_ld, h, a.qo_hd);
       reinterpret_cast<uint4*>(dst)[lane] = make_uint4(out[0], out[1], out[2], out[3]);
       reinterpret_cast<uint4*>(dst + D / 2)[lane] = make_uint4(out[4], out[5], out[6], out[7]);
     }
