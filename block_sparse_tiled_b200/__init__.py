@@ -19,9 +19,14 @@ and the operators of a transformer block on either side of it:
     vsa_rms_norm        RMS norm with the residual's addition, bf16 or 8-bit output
     vsa_qk_rope         head norm and multi-axis rotary positions of Q and K
     vsa_packed_attn     attention over packed whole prompts (vsa_packed_plan)
+
+Work runs on `stream` (a torch.cuda.Stream or a raw handle; by default the current stream).  What these operators
+allocate belongs to that stream, as if they were called under torch.cuda.stream(stream): their inputs have to be ready
+on it, and another stream that reads their outputs has to wait for it.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -215,6 +220,16 @@ def _stream(stream):
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
     return ctypes.c_void_p(int(stream))
+
+
+def _allocating_on(stream, device):
+    """The context in which torch allocates and fills memory for a call on `stream` of `device`: memory of that
+    stream's pool, whose earlier and later uses the stream orders (None: the current stream's, as anywhere)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
 
 
 def _ptr(t, dtype=None, name="tensor"):
@@ -632,7 +647,19 @@ def _stream_on(stream, index):
     """The raw handle of `stream`, by default the current stream of device `index`."""
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(index)
-    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+    if not isinstance(stream, torch.cuda.Stream):
+        return int(stream)
+    if stream.device_index != index:
+        raise ValueError(f"the stream is on cuda:{stream.device_index}, the tensors on cuda:{index}")
+    return stream.cuda_stream
+
+
+def _empty(shape, dtype, device, stream):
+    """An output that a call on `stream` allocates."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _allocating_on(stream, device):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _row_stride(t, shape, name):
@@ -669,7 +696,7 @@ def vsa_rms_norm(x, weight=None, eps=1e-6, residual=None, out=None, residual_out
     C = shape[-1]
     rows = x.numel() // C
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype or _BF16, device=x.device)
+        out = _empty(shape, out_dtype or _BF16, x.device, stream)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out is {out.dtype}, out_dtype is {out_dtype}")
     f8 = out.dtype == _E4M3
@@ -685,7 +712,7 @@ def vsa_rms_norm(x, weight=None, eps=1e-6, residual=None, out=None, residual_out
         w_ptr = weight.data_ptr()
     if f8:
         if scale is None:
-            scale = torch.empty(shape[:-1], dtype=_F32, device=x.device)
+            scale = _empty(shape[:-1], _F32, x.device, stream)
         elif scale.dtype != _F32:
             raise TypeError(f"scale must be torch.float32, got {scale.dtype}")
         elif scale.numel() != rows or not scale.is_contiguous():
@@ -698,7 +725,7 @@ def vsa_rms_norm(x, weight=None, eps=1e-6, residual=None, out=None, residual_out
         if not r_f32 and residual.dtype != _BF16:
             raise TypeError(f"residual must be torch.bfloat16 or torch.float32, got {residual.dtype}")
         if residual_out is None:
-            residual_out = torch.empty(shape, dtype=residual.dtype, device=x.device)
+            residual_out = _empty(shape, residual.dtype, x.device, stream)
         elif residual_out.dtype != residual.dtype:
             raise TypeError(f"residual_out must be {residual.dtype}, got {residual_out.dtype}")
         r_ptr, r_ld = residual.data_ptr(), _row_stride(residual, shape, "residual")
@@ -822,7 +849,7 @@ def vsa_qk_rope(rope, q, k, positions, q_weight=None, k_weight=None, eps=1e-6, q
     if positions.dim() < 2 or positions.shape[-1] != axes or not positions.is_contiguous():
         raise ValueError(f"positions must be a contiguous [tokens, {axes}], got {tuple(positions.shape)}")
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=_BF16, device=q.device)
+        q_out = _empty(q.shape, _BF16, q.device, stream)
     elif q_out.shape != q.shape:
         raise ValueError(f"q_out must have q's shape {tuple(q.shape)}, got {tuple(q_out.shape)}")
     _, _, qo_ld, qo_hd = _head_rows(q_out, D, "q_out")
@@ -832,7 +859,7 @@ def vsa_qk_rope(rope, q, k, positions, q_weight=None, k_weight=None, eps=1e-6, q
         if tk != tokens:
             raise ValueError(f"k has {tk} tokens, q {tokens}")
         if k_out is None:
-            k_out = torch.empty(k.shape, dtype=_BF16, device=k.device)
+            k_out = _empty(k.shape, _BF16, k.device, stream)
         elif k_out.shape != k.shape:
             raise ValueError(f"k_out must have k's shape {tuple(k.shape)}, got {tuple(k_out.shape)}")
         _, _, ko_ld, ko_hd = _head_rows(k_out, D, "k_out")
@@ -938,9 +965,10 @@ def vsa_packed_attn(plan, q, k, v, out=None, stream=None):
     if Tk != T or Tv != T:
         raise ValueError(f"q has {T} rows, k {Tk}, v {Tv}")
     if out is None:
-        out = torch.empty(q.shape, dtype=_BF16, device=q.device)
+        out = _empty(q.shape, _BF16, q.device, stream)
         if T > n:
-            out.view(T, H, D)[n:].zero_()
+            with _allocating_on(stream, q.device):
+                out.view(T, H, D)[n:].zero_()
     elif out.shape != q.shape:
         raise ValueError(f"out must have q's shape {tuple(q.shape)}, got {tuple(out.shape)}")
     _, _, o_ld, o_hd = _head_rows(out, D, "out")
