@@ -20,9 +20,9 @@ and the operators of a transformer block on either side of it:
     vsa_qk_rope         head norm and multi-axis rotary positions of Q and K
     vsa_packed_attn     attention over packed whole prompts (vsa_packed_plan)
 
-Work runs on `stream` (a torch.cuda.Stream or a raw handle; by default the current stream).  What these operators
-allocate belongs to that stream, as if they were called under torch.cuda.stream(stream): their inputs have to be ready
-on it, and another stream that reads their outputs has to wait for it.
+Work runs on `stream` (a torch.cuda.Stream or a raw handle; by default the current stream).  What a call allocates on
+the device belongs to that stream, as if it were made under torch.cuda.stream(stream): its inputs have to be ready on
+it, and another stream that reads its outputs has to wait for it.
 """
 from __future__ import annotations
 
@@ -454,7 +454,9 @@ def vsa_forward_host(plan, q, k, v, gate, out=None, workspace=None, head_chunk=N
     if workspace is None:
         cached = getattr(plan, "_host_ws", None)
         if cached is None or cached.numel() < need:
-            cached = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", torch.cuda.current_device()))
+            device = torch.device("cuda", torch.cuda.current_device())
+            with _allocating_on(stream, device):
+                cached = torch.empty(need, dtype=torch.uint8, device=device)
             plan._host_ws = cached
         workspace = cached
     if out is None:
@@ -478,10 +480,11 @@ def vsa_forward(plan, q, k, v, gate, out=None, workspace=None, stream=None):
     with `workspace` sized by host_workspace_bytes when given."""
     if not q.is_cuda:
         return vsa_forward_host(plan, q, k, v, gate, out=out, workspace=workspace, stream=stream)
-    if out is None:
-        out = torch.empty_like(q)
-    if workspace is None:
-        workspace = alloc_workspace(plan, q.device)
+    with _allocating_on(stream, q.device):
+        if out is None:
+            out = torch.empty_like(q)
+        if workspace is None:
+            workspace = alloc_workspace(plan, q.device)
     bf = torch.bfloat16
     _check(load_library().vsa_forward(
         plan.handle, _ptr(q, bf, "q"), _ptr(k, bf, "k"), _ptr(v, bf, "v"), _ptr(gate, bf, "gate"),
@@ -513,7 +516,8 @@ def vsa_forward_parts(plan, q_parts, k_parts, v_parts, gate_parts, out_parts, he
         raise ValueError("q, k, v, gate and out need the same number of parts, at most MAX_PARTS")
     B, Ls, Htot, D = q_parts[0].shape
     if workspace is None:
-        workspace = alloc_workspace(plan, q_parts[0].device)
+        with _allocating_on(stream, q_parts[0].device):
+            workspace = alloc_workspace(plan, q_parts[0].device)
     bf = torch.bfloat16
 
     def arr(ts, name):

@@ -75,3 +75,19 @@ def test_outputs_are_not_reused_while_the_calls_stream_writes_them(vsa):
         call(None)
         torch.cuda.synchronize()
         assert not reused_by_the_current_stream(call, s)
+
+
+def test_forward_allocates_on_the_calls_stream(vsa, monkeypatch):
+    plan = vsa.vsa_plan_tiles(1, 2, 64, segments=(70,), grid=(4, 8, 8), sparsity=0.5)
+    q, k, v = (randn(9 + i, 1, 70 + 256, 2, 64) for i in range(3))
+    gate = randn(12, 1, 70 + 256, 2)
+    want = vsa.vsa_forward(plan, q, k, v, gate)
+    s, at = torch.cuda.Stream(), []
+    alloc = vsa.alloc_workspace
+    monkeypatch.setattr(vsa, "alloc_workspace", lambda *a: (at.append(torch.cuda.current_stream()), alloc(*a))[1])
+    assert not reused_by_the_current_stream(lambda s: (vsa.vsa_forward(plan, q, k, v, gate, stream=s),), s)
+    torch.cuda.synchronize()
+    out = torch.zeros_like(q)
+    vsa.vsa_forward_parts(plan, [q], [k], [v], [gate], [out], 0, stream=s)
+    s.synchronize()
+    assert at == [s, s] and torch.equal(out, want)
