@@ -49,10 +49,10 @@ __device__ __forceinline__ void add2(float* d, float a0, float a1, float b0, flo
       : "=f"(d[0]), "=f"(d[1])
       : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
 }
-// Largest of three; NaNs lose.
+// Largest of three; a NaN wins.
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kWarp ? 256 : kNormThreads<kC>, kWarp ? 1 : kN
   constexpr int kWarps = kNormThreads<kC> / 32;  // of a row, at most
   __shared__ float2 part[2][kWarps];
   int slot = 0;
-  const auto most_of = [](float v) {  // over the warp, of values >= 0 (their bits are in their order)
+  const auto most_of = [](float v) {  // over the warp, of values >= 0 (their bits are in their order, a NaN's above all)
     return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
   };
   const auto reduce = [&](float* sum, float* most) {
@@ -267,7 +267,8 @@ __global__ void __launch_bounds__(kWarp ? 256 : kNormThreads<kC>, kWarp ? 1 : kN
     }
     const float rstd = rsqrtf(mean);  // of the row as t holds it (within 2 ulp)
     if constexpr (kF8) {
-      if (lane == 0) a.scale[row] = top > 0.0f ? top * rstd / 448.0f : isnan(ss) ? ss : 0.0f;
+      // (an infinite element makes top infinite, or NaN where its weight is 0, and rstd 0: the scale is NaN like max|y|)
+      if (lane == 0) a.scale[row] = top == 0.0f ? 0.0f : top * rstd / 448.0f;
       if (top < 1e-30f) {  // 448 / top may overflow: the row is raised by 2^64 (exactly)
         top *= 0x1p64f;
 #pragma unroll

@@ -414,8 +414,10 @@ vsa_status vsa_plan_workspace(vsa_plan p, vsa_workspace_layout* out);
  *                  scale rule of qk_fp8; a row of zeros has scale 0 and zero
  *                  codes; round to nearest even, saturating).  y itself is not
  *                  rounded before the division, which is carried out in binary32.
- * The mean is that of the unrounded t, held in binary32.  A row with a NaN or
- * an infinity gives NaN outputs (with out_e4m3: a NaN scale).
+ * The mean is that of the unrounded t, held in binary32.  A row of t with a
+ * NaN gives NaN outputs.  One with an infinity gives what the formula gives: NaN
+ * there, 0 at its finite elements.  With out_e4m3 a row whose y holds a NaN has
+ * a NaN scale (its codes are not specified).
  *  - width: a multiple of 8 in [8, 16384]; any number of rows, 0 included.
  *  - strides: elements between rows, multiples of 8; an input's may be 0 (one
  *    row for all) or any, an output's at least the width.
