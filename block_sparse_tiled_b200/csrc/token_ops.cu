@@ -254,8 +254,9 @@ __global__ void __launch_bounds__(kWarp ? 256 : kNormThreads<kC>, kWarp ? 1 : kN
     };
     sums();
     float mean = ss / n + a.eps;
-    if (isinf(ss) || mean < 1e-30f) {  // the squares left binary32's range: once more, of the row times 2^-70 or 2^70
-      const float unit = isinf(ss) ? 0x1p-70f : 0x1p70f;
+    // The squares left binary32's range: once more, of the row times 2^-80 (squares of 16384 values below 2^48 fit) or 2^70.
+    if (isinf(ss) || mean < 1e-30f) {
+      const float unit = isinf(ss) ? 0x1p-80f : 0x1p70f;
       top = 0.0f;
 #pragma unroll
       for (int u = 0; u < kC; ++u) {

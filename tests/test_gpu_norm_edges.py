@@ -1,11 +1,12 @@
-"""vsa_rms_norm on values that are not finite, against what its formula gives."""
+"""vsa_rms_norm at the ends of binary32's range and on values that are not finite, against its formula.
+Bounds as in test_gpu_token_ops.py: half a step of the output's type, and 1e-5 for the binary32 arithmetic before it."""
 import pytest
 import torch
 
 pytestmark = pytest.mark.gpu
 
 BF16, E4M3 = torch.bfloat16, torch.float8_e4m3fn
-EPS = 1e-6
+B_HALF, E_HALF, ARITH, EPS = 2.0 ** -8, 2.0 ** -4, 1e-5, 1e-6
 INF, NAN = float("inf"), float("nan")
 
 
@@ -62,3 +63,23 @@ def test_bf16_row_with_an_infinity(vsa, width, bad):
     assert out[2, there].isnan().all() and (out[2, ~there] == 0).all()
     assert out[4].isnan().all()
     assert torch.isfinite(out[[0, 1, 3, 5]]).all()
+
+
+@pytest.mark.parametrize("width", [64, 1024, 5120, 8200, 16384])
+@pytest.mark.parametrize("lo,hi", [(2.0e38, 3.3e38), (1.0e19, 4.0e19), (1.2e17, 1.6e17)])
+def test_wide_rows_near_the_largest_number(vsa, width, lo, hi):
+    """Rows that are finite, however large and wide, and however far the sum of their squares is out of range."""
+    g = torch.Generator(device="cuda").manual_seed(width)
+    size = torch.empty(5, width, device="cuda").uniform_(lo, hi, generator=g)
+    r = torch.where(torch.rand(5, width, generator=g, device="cuda") < 0.5, size, -size)
+    x, w = torch.zeros(5, width, dtype=BF16, device="cuda"), randn(7, width)
+    t = r.double()
+    y = t / torch.sqrt((t * t).mean(-1, keepdim=True) + EPS) * w.double()
+    out, _, res = vsa.vsa_rms_norm(x, w, EPS, residual=r)
+    assert torch.equal(res, r)
+    assert ((out.double() - y).abs() <= (B_HALF + 2 * ARITH) * y.abs()).all()
+    codes, scale, _ = vsa.vsa_rms_norm(x, w, EPS, residual=r, out_dtype=E4M3)
+    want = y.abs().amax(-1) / 448.0
+    s = scale.double()[:, None]
+    assert ((scale.double() - want).abs() <= ARITH * want).all()
+    assert ((codes.double() * s - y).abs() <= (E_HALF + 4 * ARITH) * y.abs() + 2.0 ** -10 * (1 + ARITH) * s).all()
