@@ -841,8 +841,8 @@ def _head_weight(w, D, name):
 def vsa_qk_rope(rope, q, k, positions, q_weight=None, k_weight=None, eps=1e-6, q_out=None, k_out=None, stream=None):
     """Head norm (with q_weight / k_weight [D]) and rotary positions of q [T, H, D] and k [T, Hk, D] (or
     [B, L, H, D]; any token and head strides that are multiples of 8, e.g. slices of one projection; k may be
-    None), bf16.  positions: [T, n_axes] int32 or float32, or [L, n_axes] for a batch of B sequences.  In place
-    with q_out = q, k_out = k.  Returns (q_out, k_out)."""
+    None), bf16.  positions: [T, n_axes] int32 or float32 (any leading dimensions of T rows in all), or for q
+    [B, L, H, D] the [L, n_axes] that every sequence uses.  In place with q_out = q, k_out = k.  Returns (q_out, k_out)."""
     D, axes = rope.head_dim, rope.n_axes
     index = _launch_index(("q", "k", "positions", "q_weight", "k_weight", "q_out", "k_out"), q, k, positions, q_weight,
                           k_weight, q_out, k_out)
@@ -852,6 +852,11 @@ def vsa_qk_rope(rope, q, k, positions, q_weight=None, k_weight=None, eps=1e-6, q
         raise TypeError(f"positions must be torch.int32 or torch.float32, got {positions.dtype}")
     if positions.dim() < 2 or positions.shape[-1] != axes or not positions.is_contiguous():
         raise ValueError(f"positions must be a contiguous [tokens, {axes}], got {tuple(positions.shape)}")
+    rows = positions.numel() // axes
+    # the library repeats any number of rows that divides the tokens (and refuses others); here only a batch's sequences do
+    if rows != tokens and not (q.dim() == 4 and rows == q.shape[1]) and rows > 0 and tokens % rows == 0:
+        fits = f"{tokens}" if q.dim() == 3 else f"{q.shape[1]} or {tokens}"
+        raise ValueError(f"positions must have {fits} rows for q {tuple(q.shape)}, got {rows}")
     if q_out is None:
         q_out = _empty(q.shape, _BF16, q.device, stream)
     elif q_out.shape != q.shape:
@@ -870,7 +875,7 @@ def vsa_qk_rope(rope, q, k, positions, q_weight=None, k_weight=None, eps=1e-6, q
         k_ptr, ko_ptr = k.data_ptr(), k_out.data_ptr()
     elif k_out is not None or k_weight is not None:
         raise ValueError("k_out and k_weight need k")
-    a = QkRopeArgs(tokens, positions.numel() // axes, H, Hk, pos_f32, eps, positions.data_ptr(), q.data_ptr(), k_ptr,
+    a = QkRopeArgs(tokens, rows, H, Hk, pos_f32, eps, positions.data_ptr(), q.data_ptr(), k_ptr,
                    q_out.data_ptr(), ko_ptr, 0 if q_weight is None else _head_weight(q_weight, D, "q_weight"),
                    0 if k_weight is None else _head_weight(k_weight, D, "k_weight"), q_ld, q_hd, k_ld, k_hd, qo_ld,
                    qo_hd, ko_ld, ko_hd)

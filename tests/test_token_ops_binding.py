@@ -1,0 +1,53 @@
+"""Refusals of the token operators' Python binding that need no GPU: the checks that come before anything is launched,
+with CPU tensors standing in for CUDA ones where the device check is replaced."""
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def vsa():
+    from block_sparse_tiled_b200 import build
+
+    build.build()
+    import block_sparse_tiled_b200 as m
+
+    m.load_library()
+    return m
+
+
+class Launched(Exception):
+    """Every check of the binding has passed."""
+
+
+@pytest.fixture
+def no_device(vsa, monkeypatch):
+    def launch(*_):
+        raise Launched
+
+    monkeypatch.setattr(vsa, "_launch_index", lambda *_: 0)
+    monkeypatch.setattr(vsa, "_stream_on", launch)
+    return vsa
+
+
+def bf16(*shape):
+    return torch.zeros(*shape, dtype=torch.bfloat16)
+
+
+@pytest.mark.parametrize("q,rows", [
+    ((100, 2, 64), 50), ((100, 2, 64), 1), ((100, 2, 64), 25),  # [T, H, D] takes a row for every token
+    ((2, 30, 2, 64), 2), ((2, 30, 2, 64), 15), ((2, 30, 2, 64), 1), ((4, 1, 2, 64), 2),  # [B, L, H, D]: L or B * L
+])
+def test_positions_that_would_be_used_for_other_tokens(no_device, q, rows):
+    rope = no_device.vsa_rope_create(64, (16, 16))
+    for k in (None, bf16(*q)):
+        with pytest.raises(ValueError, match="positions"):
+            no_device.vsa_qk_rope(rope, bf16(*q), k, torch.zeros(rows, 2, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("q,pos", [((100, 2, 64), (100, 2)), ((2, 30, 2, 64), (30, 2)), ((2, 30, 2, 64), (60, 2)),
+                                   ((2, 30, 2, 64), (2, 30, 2)), ((2, 30, 2, 64), (1, 30, 2)), ((1, 2, 64), (1, 2)),
+                                   ((4, 1, 2, 64), (1, 2)), ((0, 2, 64), (0, 2))])
+def test_positions_that_fit(no_device, q, pos):
+    rope = no_device.vsa_rope_create(64, (16, 16))
+    with pytest.raises(Launched):
+        no_device.vsa_qk_rope(rope, bf16(*q), None, torch.zeros(*pos, dtype=torch.int32))
