@@ -12,6 +12,7 @@
 #include <new>
 #include <type_traits>
 
+#include "rows.h"
 #include "status.h"
 #include "vsa.h"
 
@@ -563,13 +564,17 @@ vsa_status check_ptr(const char* what, const void* p) {
   return VSA_OK;
 }
 
-// In place means the same rows: an output that starts where an input starts has its strides.
-vsa_status check_alias(const char* what, const void* in, int64_t in_ld, const void* out, int64_t out_ld, int64_t rows,
-                       bool same_type) {
-  if (in != out || in == nullptr) return VSA_OK;
-  if (!same_type || (rows > 1 && in_ld != out_ld))
-    return set_error(VSA_ERR_INVALID_ARG, "%s: an output in place of an input needs its type and stride", what);
-  return VSA_OK;
+// An output may lie over an operand only where it replaces an input row for row.
+struct Operand {
+  const char* name;
+  vsa::Rows rows;  // base NULL: not given
+};
+vsa_status check_overlap(const Operand& out, const Operand& other, bool may_replace) {
+  if (out.rows.base == nullptr || other.rows.base == nullptr || (may_replace && vsa::same_rows(out.rows, other.rows)) ||
+      !vsa::rows_meet(out.rows, other.rows))
+    return VSA_OK;
+  return set_error(VSA_ERR_INVALID_ARG, "%s lies over %s%s", out.name, other.name,
+                   may_replace ? " but does not replace it row for row (same address, type and strides)" : "");
 }
 
 }  // namespace
@@ -609,15 +614,24 @@ vsa_status vsa_rms_norm(const vsa_rms_norm_args* p, void* stream) {
   if (p->residual_out != nullptr) {
     VSA_TRY(check_ptr("residual_out", p->residual_out));
     VSA_TRY(check_stride("residual_out", p->rows, p->residual_out_stride, p->width, true));
-    if (p->residual_out == p->out) return set_error(VSA_ERR_INVALID_ARG, "out and residual_out are the same buffer");
   }
-  VSA_TRY(check_alias("out", p->x, p->x_stride, p->out, p->out_stride, p->rows, !p->out_e4m3));
-  VSA_TRY(check_alias("out", p->residual, p->residual_stride, p->out, p->out_stride, p->rows,
-                      !p->out_e4m3 && !p->residual_f32));
-  VSA_TRY(check_alias("residual_out", p->x, p->x_stride, p->residual_out, p->residual_out_stride, p->rows,
-                      !p->residual_f32));
-  VSA_TRY(check_alias("residual_out", p->residual, p->residual_stride, p->residual_out, p->residual_out_stride, p->rows,
-                      true));
+  const auto rows_of = [&](const char* name, const void* base, int64_t ld, int size) {
+    return Operand{name, {base, p->rows, ld * size, 1, 0, static_cast<int64_t>(p->width) * size}};
+  };
+  const auto flat = [](const char* name, const void* base, int64_t bytes) { return Operand{name, {base, 1, 0, 1, 0, bytes}}; };
+  const int res_size = p->residual_f32 ? 4 : 2;
+  const Operand x = rows_of("x", p->x, p->x_stride, 2), residual = rows_of("residual", p->residual, p->residual_stride, res_size);
+  const Operand weight = flat("weight", p->weight, static_cast<int64_t>(p->width) * (p->weight_f32 ? 4 : 2));
+  const Operand out = rows_of("out", p->out, p->out_stride, p->out_e4m3 ? 1 : 2);
+  const Operand res_out = rows_of("residual_out", p->residual_out, p->residual_out_stride, res_size);
+  const Operand scale = flat("scale", p->out_e4m3 ? p->scale : nullptr, 4 * p->rows);
+  for (const Operand* o : {&out, &res_out}) {
+    VSA_TRY(check_overlap(*o, x, true));
+    VSA_TRY(check_overlap(*o, residual, true));
+    VSA_TRY(check_overlap(*o, weight, false));
+  }
+  VSA_TRY(check_overlap(out, res_out, false));
+  for (const Operand* o : {&x, &residual, &weight, &out, &res_out}) VSA_TRY(check_overlap(scale, *o, false));
   NormArgs a = {};
   a.x = p->x;
   a.residual = p->residual;
@@ -742,6 +756,9 @@ vsa_status vsa_qk_rope(vsa_rope r, const vsa_qk_rope_args* p, void* stream) {
     return set_error(VSA_ERR_SHAPE, "pos_rows must divide the %lld tokens, got %lld", static_cast<long long>(p->tokens),
                      static_cast<long long>(p->pos_rows));
   VSA_TRY(check_ptr("positions", p->positions));
+  const auto rows_of = [&](const char* name, const void* base, int heads, int64_t ld, int64_t hd) {
+    return Operand{name, {base, p->tokens, ld * 2, heads, hd * 2, D * 2}};
+  };
   const auto check = [&](const char* what, int heads, const void* in, int64_t ld, int64_t hd, const void* out,
                          int64_t old, int64_t ohd, const void* w) -> vsa_status {
     VSA_TRY(check_ptr(what, in));
@@ -751,19 +768,34 @@ vsa_status vsa_qk_rope(vsa_rope r, const vsa_qk_rope_args* p, void* stream) {
     VSA_TRY(check_stride(what, heads, hd, D, false));
     VSA_TRY(check_stride(what, p->tokens, old, D, true));
     VSA_TRY(check_stride(what, heads, ohd, D, true));
-    // rows of the output must be disjoint: heads inside a token's stride, or tokens inside a head's
-    if (p->tokens > 1 && heads > 1 && old < (heads - 1) * ohd + D && ohd < (p->tokens - 1) * old + D)
+    if (!vsa::rows_disjoint(rows_of(what, out, heads, old, ohd).rows))
       return set_error(VSA_ERR_SHAPE, "%s: the output's rows overlap", what);
-    if (in == out && ((p->tokens > 1 && ld != old) || (heads > 1 && hd != ohd)))
-      return set_error(VSA_ERR_INVALID_ARG, "%s: an output in place of the input needs its strides", what);
     return VSA_OK;
   };
   VSA_TRY(check("q", p->heads, p->q, p->q_stride, p->q_head_stride, p->q_out, p->q_out_stride, p->q_out_head_stride,
                 p->q_weight));
-  if (p->kv_heads > 0 && p->k_out == p->q_out) return set_error(VSA_ERR_INVALID_ARG, "q_out and k_out are the same buffer");
   if (p->kv_heads > 0)
     VSA_TRY(check("k", p->kv_heads, p->k, p->k_stride, p->k_head_stride, p->k_out, p->k_out_stride,
                   p->k_out_head_stride, p->k_weight));
+  {
+    const bool with_k = p->kv_heads > 0;
+    const auto flat = [](const char* name, const void* base, int64_t bytes) { return Operand{name, {base, 1, 0, 1, 0, bytes}}; };
+    const Operand q = rows_of("q", p->q, p->heads, p->q_stride, p->q_head_stride);
+    const Operand q_out = rows_of("q_out", p->q_out, p->heads, p->q_out_stride, p->q_out_head_stride);
+    const Operand k = rows_of("k", with_k ? p->k : nullptr, p->kv_heads, p->k_stride, p->k_head_stride);
+    const Operand k_out = rows_of("k_out", with_k ? p->k_out : nullptr, p->kv_heads, p->k_out_stride, p->k_out_head_stride);
+    const Operand shared[] = {flat("q_weight", p->q_weight, 2 * D), flat("k_weight", with_k ? p->k_weight : nullptr, 2 * D),
+                              flat("positions", p->positions, p->pos_rows * r->n_axes * 4)};
+    VSA_TRY(check_overlap(q_out, q, true));
+    VSA_TRY(check_overlap(k_out, k, true));
+    VSA_TRY(check_overlap(q_out, k, false));
+    VSA_TRY(check_overlap(k_out, q, false));
+    VSA_TRY(check_overlap(q_out, k_out, false));
+    for (const Operand& o : shared) {
+      VSA_TRY(check_overlap(q_out, o, false));
+      VSA_TRY(check_overlap(k_out, o, false));
+    }
+  }
   RopeArgs a = {};
   a.q = p->q;
   a.k = p->k;

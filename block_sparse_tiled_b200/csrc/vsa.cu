@@ -21,6 +21,7 @@
 #include "attn_sm100.cuh"
 #include "packed_attn_sm100.cuh"
 #include "prep_kernels.cuh"
+#include "rows.h"
 #include "status.h"
 #include "vsa.h"
 
@@ -1663,9 +1664,8 @@ vsa_status check_packed_strides(const char* what, int64_t tokens, int64_t heads,
   for (const int64_t x : {ld, hd})
     if (x < 0 || (x & 7) != 0 || x >= (int64_t(1) << 39))
       return fail(VSA_ERR_INVALID_ARG, std::string(what) + ": strides must be non-negative multiples of 8 elements");
-  const bool token_major = (heads == 1 || hd >= D) && (tokens == 1 || ld >= (heads - 1) * hd + D);
-  const bool head_major = (tokens == 1 || ld >= D) && (heads == 1 || hd >= (tokens - 1) * ld + D);
-  if (output && !token_major && !head_major) return fail(VSA_ERR_SHAPE, std::string(what) + ": its rows overlap");
+  if (output && !vsa::rows_disjoint({nullptr, tokens, ld * 2, heads, hd * 2, D * 2}))
+    return fail(VSA_ERR_SHAPE, std::string(what) + ": its rows overlap");
   return VSA_OK;
 }
 
@@ -1794,9 +1794,16 @@ vsa_status vsa_packed_attn(vsa_packed_plan_t p, const vsa_packed_args* a, void* 
     VSA_TRY(check_packed_strides("k", n, p->kv_heads, p->D, a->k_stride, a->k_head_stride, false));
     VSA_TRY(check_packed_strides("v", n, p->kv_heads, p->D, a->v_stride, a->v_head_stride, false));
     VSA_TRY(check_packed_strides("out", n, p->heads, p->D, a->out_stride, a->out_head_stride, true));
-    if (a->out == a->k || a->out == a->v) return fail(VSA_ERR_INVALID_ARG, "out must not overlap k or v");
-    if (a->out == a->q && (a->out_stride != a->q_stride || a->out_head_stride != a->q_head_stride))
-      return fail(VSA_ERR_INVALID_ARG, "out over q needs q's strides");
+    const auto rows_of = [&](const void* base, int64_t heads, int64_t ld, int64_t hd) {
+      return vsa::Rows{base, n, ld * 2, heads, hd * 2, p->D * 2};
+    };
+    const vsa::Rows out = rows_of(a->out, p->heads, a->out_stride, a->out_head_stride);
+    const vsa::Rows q = rows_of(a->q, p->heads, a->q_stride, a->q_head_stride);
+    if (vsa::rows_meet(out, rows_of(a->k, p->kv_heads, a->k_stride, a->k_head_stride)) ||
+        vsa::rows_meet(out, rows_of(a->v, p->kv_heads, a->v_stride, a->v_head_stride)))
+      return fail(VSA_ERR_INVALID_ARG, "out must not overlap k or v");
+    if (vsa::rows_meet(out, q) && !vsa::same_rows(out, q))
+      return fail(VSA_ERR_INVALID_ARG, "out over q has to replace it row for row (same address and strides)");
     const int g = p->heads / p->kv_heads, tb = p->dims.tile_tokens;
     CUtensorMap mq, mk, mv;
     VSA_TRY(make_packed_map(&mq, a->q, n, p->heads, p->D, a->q_stride, a->q_head_stride, g, tb));

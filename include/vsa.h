@@ -423,7 +423,8 @@ vsa_status vsa_plan_workspace(vsa_plan p, vsa_workspace_layout* out);
  *    row for all) or any, an output's at least the width.
  *  - In place: out may be x or residual, residual_out may be residual or x (of
  *    the same type and stride); otherwise outputs must not overlap inputs or
- *    one another.
+ *    one another (VSA_ERR_INVALID_ARG: rows in one address range count as
+ *    overlapping unless they keep equal strides and lie beside one another).
  * No plan and no workspace: calls on different streams may overlap, and a call
  * may be captured.  The current device must be the one that holds the tensors.
  * Errors: VSA_ERR_INVALID_ARG, VSA_ERR_SHAPE, VSA_ERR_UNSUPPORTED, VSA_ERR_CUDA. */
@@ -484,7 +485,7 @@ vsa_status vsa_rope_destroy(vsa_rope r);
  *  - strides: elements between tokens and between heads, multiples of 8, so q
  *    and k may be slices of one projection; output rows must not overlap.
  *  - In place: q_out may be q and k_out may be k (same strides); otherwise
- *    outputs must not overlap inputs.
+ *    outputs must not overlap inputs or one another (refused as above).
  * No workspace: calls may overlap on the GPU and may be captured.  The current
  * device must be the one that holds the tensors.
  * Errors: VSA_ERR_INVALID_ARG, VSA_ERR_SHAPE, VSA_ERR_CUDA. */
@@ -519,7 +520,8 @@ vsa_status vsa_qk_rope(vsa_rope r, const vsa_qk_rope_args* args, void* stream);
  *  - q, out [tokens, heads, head_dim], k, v [tokens, kv_heads, head_dim] with
  *    any token and head strides that are multiples of 8 elements; tokens >=
  *    the lengths' sum.  Rows behind the last sequence are neither read nor
- *    written.  out may be q (same strides); it must not overlap k or v.
+ *    written.  out may be q (same strides); it must not overlap k or v, or q
+ *    in another way (refused as above).
  *  - A sequence's output depends on its own rows only, whatever the others
  *    hold.  Inside one, a masked key's score is replaced, so NaN or infinite
  *    keys stay where they are seen; a NaN or infinite value v[j] may also reach
