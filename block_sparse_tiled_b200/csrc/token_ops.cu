@@ -453,7 +453,10 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) qk_rope_kernel(const 
       float mean = mean_square(), eps = a.eps;
       const bool far = weight != nullptr && (isinf(mean) || mean + eps < 1e-30f);
       if (__any_sync(0xffffffffu, far)) {  // squares outside binary32's range: once more, of the row times 2^-70 or 2^70
-        const float unit = !far ? 1.0f : isinf(mean) ? 0x1p-70f : 0x1p70f;
+        // (for all lanes of a row alike: six lanes add in different orders, and at the border their sums may disagree)
+        const uint32_t row = ((1u << kLanes) - 1) << (wl - lane);
+        const bool over = (__ballot_sync(0xffffffffu, isinf(mean)) & row) != 0;
+        const float unit = (__ballot_sync(0xffffffffu, far) & row) == 0 ? 1.0f : over ? 0x1p-70f : 0x1p70f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) raw[j] = pack2(low(raw[j]) * unit, high(raw[j]) * unit);
         eps = eps * unit * unit;  // (unit squared leaves the range)
