@@ -50,7 +50,7 @@ EXPORTED = (
     "vsa_plan_workspace", "vsa_device_status", "vsa_last_error", "vsa_version",
     "vsa_rms_norm", "vsa_rope_create", "vsa_rope_table", "vsa_rope_destroy", "vsa_qk_rope",
     "vsa_packed_plan", "vsa_packed_query", "vsa_packed_info", "vsa_packed_destroy", "vsa_packed_attn",
-    "vsa_packed_status",
+    "vsa_packed_status", "vsa_packed_wait_selftest",
 )
 
 
@@ -202,6 +202,8 @@ def load_library(path: str = LIB_PATH):
     lib.vsa_packed_destroy.argtypes = [P]
     lib.vsa_packed_attn.argtypes = [P, ctypes.POINTER(PackedArgs), P]
     lib.vsa_packed_status.argtypes = [P, P, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int32)]
+    lib.vsa_packed_wait_selftest.argtypes = [P, ctypes.c_int64, P, ctypes.POINTER(ctypes.c_int32),
+                                             ctypes.POINTER(ctypes.c_int32)]
     for name in EXPORTED:
         if name not in ("vsa_last_error", "vsa_version"):
             getattr(lib, name).restype = st
@@ -937,6 +939,14 @@ class PackedPlan:
         code, where = ctypes.c_int32(), ctypes.c_int32()
         _check(load_library().vsa_packed_status(self.handle, _stream(stream), ctypes.byref(code), ctypes.byref(where)),
                "vsa_packed_status")
+        return code.value, where.value
+
+    def wait_selftest(self, timeout_ns=50_000_000, stream=None):
+        """Run the packed attention's bounded-wait self-test; returns the (code, site) it recorded."""
+        code, where = ctypes.c_int32(), ctypes.c_int32()
+        _check(load_library().vsa_packed_wait_selftest(self.handle, int(timeout_ns), _stream(stream),
+                                                       ctypes.byref(code), ctypes.byref(where)),
+               "vsa_packed_wait_selftest")
         return code.value, where.value
 
     def destroy(self):

@@ -114,17 +114,19 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
   return d;
 }
 
-// mbar_wait and mbar_wait_drain without a call (the softmax's registers would be saved around it): every 1024 looks
-// the abort flag and the time.  With kIdle, for the warps that run ahead, kIdleNs of sleep between looks.
+// mbar_wait and mbar_wait_drain without a call (the softmax's registers would be saved around it): the abort flag at the
+// first look that fails and at every eighth, the time at every 1024th.  With kIdle, for the warps that run ahead, kIdleNs
+// of sleep between looks.
 constexpr unsigned kIdleNs = 100;
 template <bool kIdle = false>
 __device__ __forceinline__ bool packed_wait(uint64_t* bar, uint32_t parity, const WaitCtl& ctl, int site,
                                             bool drain = false) {
   uint64_t t0 = 0;
-  for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it) {
+  for (uint32_t it = 0; !mbar_try_wait(bar, parity); ++it) {
     if (kIdle) __nanosleep(kIdleNs);
-    if ((it & 1023u) != 0) continue;
+    if ((it & 7u) != 0) continue;
     if (!drain && *ctl.abort_flag) return false;
+    if ((it & 1016u) != 1016u) continue;
     const uint64_t now = globaltimer_ns();
     if (t0 == 0) t0 = now;
     if (now - t0 > ctl.timeout_ns) {
@@ -134,6 +136,28 @@ __device__ __forceinline__ bool packed_wait(uint64_t* bar, uint32_t parity, cons
     }
   }
   return true;
+}
+
+// Self-test of packed_wait, both forms, on a barrier that nothing arrives on: site 240 + warp if the wait ran out (or saw
+// the other warp's abort) and every later wait returned at once, 242 + warp if those took longer than one limit.
+__global__ void packed_wait_selftest_kernel(int* status, uint64_t timeout_ns) {
+  __shared__ uint64_t bar;
+  __shared__ int abort_flag;
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    mbar_init(&bar, 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  const WaitCtl ctl{&abort_flag, status, timeout_ns};
+  const auto wait = [&]() {
+    return warp == 0 ? packed_wait(&bar, 0, ctl, 240) : packed_wait<true>(&bar, 0, ctl, 241);  // phase 0 never completes
+  };
+  bool done = wait();
+  const uint64_t t0 = globaltimer_ns();
+  for (int i = 0; i < 1000; ++i) done = wait() || done;
+  if (done || globaltimer_ns() - t0 > timeout_ns) atomicExch(status + 1, 242 + warp);
 }
 
 // One thread of a converged warp, the same at every call.
@@ -379,6 +403,11 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
     float2* sum_s = reinterpret_cast<float2*>(sm + Ly::oSum);
     uint32_t g = 0;  // blocks so far, of both groups
 
+    // Once a wait of the CTA has given up, nothing that follows is worth storing: both groups look at the abort flag
+    // before they store or rescale and at the end of an item, and leave.  Until then every wait that is not ready
+    // returns at its first look, a few microseconds a block.  (A look in every block: 378 -> 386 us on the ragged D = 64
+    // batch; these 381.)
+    const auto gave_up = [&]() { return __any_sync(0xffffffffu, *abort_flag != 0) != 0; };
     // (what little lives through the block loop is recomputed or packed: a row of scores leaves 40 registers)
     // item n - 1 is complete: this group's half of its O columns, over both groups' sums
     int pending = 0;  // 0: stored; 1 + parity of its last block
@@ -393,6 +422,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
       const float2* sums = sum_s + ((n - 1) & 1) * 256;
       const float2 s0 = sums[r], s1 = sums[128 + r];
       packed_wait(&bars[Ly::bOFull], (n - 1) & 1, ctl, 233);
+      if (gave_up()) return;
       tc_fence_after();
       // O is relative to the maximum after the last block; a group without blocks has sum 0
       const float m = odd ? s1.y : s0.y;
@@ -473,6 +503,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
           if (pending) epilogue(i - i0);
           packed_wait(&bars[Ly::bPEmpty + x], use ^ 1, ctl, 238);  // two blocks back, so that the next parity is the last block's
           packed_wait(&bars[Ly::bPEmpty + ((g - 1) & 1)], ((g - 1) >> 1) & 1, ctl, 236);
+          if (gave_up()) break;
           tc_fence_after();
           const float f = raise ? ex2_approx(before - m) : 1.0f;
 #pragma unroll 1
@@ -524,6 +555,7 @@ __global__ void __launch_bounds__(kPackedThreads, 1)
         mbar_arrive(&bars[Ly::bPFull + x]);
         if (pending) epilogue(i - i0);  // the item before: its last product has run meanwhile, and this item's wait for it
       }
+      if (gave_up()) break;
       if (pending) epilogue(i - i0);  // no block of this item was this group's
       sum_s[((i - i0) & 1) * 256 + x * 128 + r] =
           make_float2((l[0] + l[1]) + (l[2] + l[3]), lm);

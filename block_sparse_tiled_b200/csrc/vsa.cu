@@ -1855,4 +1855,23 @@ vsa_status vsa_packed_status(vsa_packed_plan_t p, void* stream, int32_t* code, i
   }
 }
 
+vsa_status vsa_packed_wait_selftest(vsa_packed_plan_t p, int64_t timeout_ns, void* stream, int32_t* code,
+                                    int32_t* where) {
+  if (p == nullptr) return vsa::set_error(VSA_ERR_INVALID_ARG, "plan is NULL");
+  if (timeout_ns < 1000 || timeout_ns > 10000000000ll)
+    return vsa::set_error(VSA_ERR_INVALID_ARG, "timeout_ns must lie in [1e3, 1e10]");
+  try {
+    int dev = -1;
+    VSA_CUDA_TRY(cudaGetDevice(&dev));
+    if (dev != p->device) return fail(VSA_ERR_INVALID_ARG, "the current device is not the plan's device");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    VSA_CUDA_TRY(cudaMemsetAsync(p->d_status, 0, 2 * sizeof(int), s));
+    vsa::packed_wait_selftest_kernel<<<1, 64, 0, s>>>(p->d_status, static_cast<uint64_t>(timeout_ns));
+    VSA_TRY(launch_check("packed wait self-test"));
+    return vsa_packed_status(p, stream, code, where);
+  } catch (const std::exception&) {
+    return vsa::set_error(VSA_ERR_INVALID_ARG, "out of host memory");
+  }
+}
+
 }  // extern "C"

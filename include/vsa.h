@@ -564,6 +564,12 @@ typedef struct vsa_packed_args {
 vsa_status vsa_packed_attn(vsa_packed_plan_t p, const vsa_packed_args* args, void* stream);
 /* Read (synchronising `stream`) and clear the plan's device status word, as vsa_device_status. */
 vsa_status vsa_packed_status(vsa_packed_plan_t p, void* stream, int32_t* code, int32_t* where);
+/* Failure-detection self-test of the packed attention's own bounded wait, as vsa_wait_selftest: one small
+ * kernel waits on a barrier that nothing arrives on, with a limit of timeout_ns (1e3 .. 1e10).  A working
+ * build returns VSA_OK with *code == VSA_ERR_TIMEOUT and *where 240 or 241 after about timeout_ns; 242 or 243
+ * mean that waits after the abort did not return at once. */
+vsa_status vsa_packed_wait_selftest(vsa_packed_plan_t p, int64_t timeout_ns, void* stream, int32_t* code,
+                                    int32_t* where);
 
 /* Failure-detection self-test.  No counterpart on the pages: it checks the
  * library's own safety net.  It launches one small kernel whose threads wait,
