@@ -918,8 +918,24 @@ def vsa_packed_query(lengths, heads, kv_heads=None, head_dim=128, causal=True, s
     return dict(d.as_dict(), items=items[:d.items], first=first)
 
 
+# Handles of packed plans that were collected.  The garbage collector may run while some stream is captured, and
+# vsa_packed_destroy synchronises the device, which would end that capture: they wait here for a call that may.
+_collected_plans = []
+
+
+def _free_collected_plans():
+    while True:
+        try:
+            handle = _collected_plans.pop()
+        except IndexError:  # empty, here or by another thread
+            return
+        load_library().vsa_packed_destroy(handle)
+
+
 class PackedPlan:
-    """Owns a ``vsa_packed_plan_t`` handle: the lengths of packed sequences and the schedule made from them."""
+    """Owns a ``vsa_packed_plan_t`` handle: the lengths of packed sequences and the schedule made from them.  destroy()
+    frees it at once, after the device's work (so not during a capture); a plan that is collected is freed by the next
+    vsa_packed_plan or destroy()."""
 
     def __init__(self, handle, heads, kv_heads, head_dim, causal):
         self._h = handle
@@ -950,20 +966,20 @@ class PackedPlan:
         return code.value, where.value
 
     def destroy(self):
+        _free_collected_plans()
         if self._h is not None:
             load_library().vsa_packed_destroy(self._h)
             self._h = None
 
     def __del__(self):
-        try:
-            self.destroy()
-        except Exception:
-            pass
+        if getattr(self, "_h", None) is not None:
+            _collected_plans.append(self._h)
 
 
 def vsa_packed_plan(lengths, heads, kv_heads=None, head_dim=128, causal=True, softmax_scale=0.0, stream=None) -> PackedPlan:
     """A plan for attention over sequences of these lengths packed end to end (0 allowed), for heads query heads
     and kv_heads key heads (heads / kv_heads query heads share one, in order)."""
+    _free_collected_plans()
     desc, keep = make_packed_desc(lengths, heads, kv_heads, head_dim, causal, softmax_scale)
     h = ctypes.c_void_p()
     _check(load_library().vsa_packed_plan(ctypes.byref(desc), _stream(stream), ctypes.byref(h)), "vsa_packed_plan")

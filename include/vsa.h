@@ -553,7 +553,7 @@ vsa_status vsa_packed_plan(const vsa_packed_desc* desc, void* stream, vsa_packed
 vsa_status vsa_packed_query(const vsa_packed_desc* desc, int32_t sms, vsa_packed_dims* out, int32_t* items,
                             int32_t* first);
 vsa_status vsa_packed_info(vsa_packed_plan_t p, vsa_packed_dims* out);
-vsa_status vsa_packed_destroy(vsa_packed_plan_t p); /* synchronises with the device first */
+vsa_status vsa_packed_destroy(vsa_packed_plan_t p); /* synchronises with the device first: not during a capture */
 typedef struct vsa_packed_args {
   int64_t tokens; /* rows of q, k, v and out, >= the plan's tokens */
   const vsa_bf16 *q, *k, *v;

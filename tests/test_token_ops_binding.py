@@ -51,3 +51,51 @@ def test_positions_that_fit(no_device, q, pos):
     rope = no_device.vsa_rope_create(64, (16, 16))
     with pytest.raises(Launched):
         no_device.vsa_qk_rope(rope, bf16(*q), None, torch.zeros(*pos, dtype=torch.int32))
+
+
+class FakeLibrary:
+    """Handles without a device; the calls made, in order."""
+
+    def __init__(self, vsa):
+        self.calls, self.next = [], 100
+
+    def vsa_packed_plan(self, desc, stream, out):
+        out._obj.value = self.next
+        self.next += 1
+        self.calls.append(("plan", out._obj.value))
+        return 0
+
+    def vsa_packed_info(self, handle, dims):
+        return 0
+
+    def vsa_packed_destroy(self, handle):
+        self.calls.append(("destroy", handle.value))
+        return 0
+
+
+def test_a_collected_plan_is_freed_by_the_next_call_that_may(vsa, monkeypatch):
+    """The garbage collector may run while another stream is captured, and freeing a plan synchronises the device, which
+    would end the capture: a plan that is collected waits for the next plan (made outside of captures) or destroy()."""
+    import gc
+
+    lib = FakeLibrary(vsa)
+    monkeypatch.setattr(vsa, "load_library", lambda *_: lib)
+    monkeypatch.setattr(vsa, "_stream", lambda *_: None)
+    a = vsa.vsa_packed_plan((5,), 1)
+    b = vsa.vsa_packed_plan((6,), 1)
+    c = vsa.vsa_packed_plan((7,), 1)
+    del a
+    gc.collect()
+    assert lib.calls == [("plan", 100), ("plan", 101), ("plan", 102)]
+    d = vsa.vsa_packed_plan((8,), 1)
+    assert sorted(lib.calls[3:]) == [("destroy", 100), ("plan", 103)]
+    del b, d
+    gc.collect()
+    assert len(lib.calls) == 5
+    c.destroy()  # at once, and what waits with it
+    assert sorted(lib.calls[5:]) == [("destroy", 101), ("destroy", 102), ("destroy", 103)]
+    c.destroy()
+    del c
+    gc.collect()
+    vsa.vsa_packed_plan((9,), 1).destroy()
+    assert lib.calls[8:] == [("plan", 104), ("destroy", 104)]
