@@ -627,6 +627,14 @@ def workspace_views(plan, workspace):
 _BF16, _F32, _E4M3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
 
 
+def _int32(x, name):
+    """x as the library's 32-bit field takes it (ctypes would drop the bits above)."""
+    x = int(x)
+    if not -0x80000000 <= x <= 0x7fffffff:
+        raise ValueError(f"{name} must fit 32 bits, got {x}")
+    return x
+
+
 def _launch_index(names, *tensors):
     """The index of the one CUDA device that holds every given tensor, which must be the current device (the
     library launches there).  These calls are a few microseconds of GPU work at their smallest, so the checks
@@ -699,7 +707,7 @@ def vsa_rms_norm(x, weight=None, eps=1e-6, residual=None, out=None, residual_out
     shape = x.shape
     if not shape or shape[-1] == 0:
         raise ValueError(f"x must end in a dimension that is not empty, got {tuple(shape)}")
-    C = shape[-1]
+    C = _int32(shape[-1], "the width")
     rows = x.numel() // C
     if out is None:
         out = _empty(shape, out_dtype or _BF16, x.device, stream)
@@ -785,24 +793,24 @@ def vsa_rope_create(head_dim, sections=None, theta=10000.0, interleaved=False, s
     theta^(-i / n) radians per step, with shared_ladder pair p of the head theta^(-p / (head_dim / 2)).  Or
     inv_freq and axis, head_dim / 2 values each, give any other table (n_axes: 1 + the largest axis).
     interleaved: pair p is elements (2p, 2p + 1), else (p, p + head_dim / 2)."""
-    d = RopeDesc(head_dim=int(head_dim), interleaved=int(bool(interleaved)), shared_ladder=int(bool(shared_ladder)),
+    d = RopeDesc(head_dim=_int32(head_dim, "head_dim"), interleaved=int(bool(interleaved)), shared_ladder=int(bool(shared_ladder)),
                  theta=float(theta))
     if (inv_freq is None) != (axis is None):
         raise ValueError("inv_freq and axis go together")
     if inv_freq is not None:
         if sections is not None:
             raise ValueError("give sections, or inv_freq and axis")
-        freq, ax = [float(f) for f in inv_freq], [int(x) for x in axis]
+        freq, ax = [float(f) for f in inv_freq], [_int32(x, "an axis") for x in axis]
         if len(freq) != d.head_dim // 2 or len(ax) != d.head_dim // 2:
             raise ValueError(f"inv_freq and axis need head_dim / 2 = {d.head_dim // 2} values each")
-        d.n_axes = int(n_axes) if n_axes is not None else 1 + max(ax)
+        d.n_axes = _int32(1 + max(ax) if n_axes is None else n_axes, "n_axes")
         keep = [(ctypes.c_double * len(freq))(*freq), (ctypes.c_int32 * len(ax))(*ax)]
         d.inv_freq = ctypes.cast(keep[0], ctypes.POINTER(ctypes.c_double))
         d.axis = ctypes.cast(keep[1], ctypes.POINTER(ctypes.c_int32))
     else:
         if sections is None:
             raise ValueError("give sections, or inv_freq and axis")
-        sec = [int(s) for s in sections]
+        sec = [_int32(s, "a section") for s in sections]
         if n_axes is not None and n_axes != len(sec):
             raise ValueError("n_axes must be the number of sections")
         d.n_axes = len(sec)
@@ -894,12 +902,11 @@ def vsa_qk_rope(rope, q, k, positions, q_weight=None, k_weight=None, eps=1e-6, q
 
 def make_packed_desc(lengths, heads, kv_heads=None, head_dim=128, causal=True, softmax_scale=0.0):
     """Build the ``vsa_packed_desc`` struct; returns (struct, keep-alive buffer)."""
-    n = [int(x) for x in lengths]
-    if any(x > 0x7fffffff for x in n):
-        raise ValueError("a length is 2^31 or more")
+    n = [_int32(x, "a length") for x in lengths]
     buf = (ctypes.c_int32 * max(1, len(n)))(*n)
-    d = PackedDesc(len(n), int(heads), int(heads if kv_heads is None else kv_heads), int(head_dim), int(bool(causal)),
-                   float(softmax_scale), ctypes.cast(buf, ctypes.POINTER(ctypes.c_int32)))
+    d = PackedDesc(len(n), _int32(heads, "heads"), _int32(heads if kv_heads is None else kv_heads, "kv_heads"),
+                   _int32(head_dim, "head_dim"), int(bool(causal)), float(softmax_scale),
+                   ctypes.cast(buf, ctypes.POINTER(ctypes.c_int32)))
     return d, buf
 
 
@@ -910,10 +917,10 @@ def vsa_packed_query(lengths, heads, kv_heads=None, head_dim=128, causal=True, s
     import numpy as np
 
     desc, keep = make_packed_desc(lengths, heads, kv_heads, head_dim, causal, softmax_scale)
-    d, lib = PackedDims(), load_library()
-    _check(lib.vsa_packed_query(ctypes.byref(desc), int(sms), ctypes.byref(d), None, None), "vsa_packed_query")
+    d, lib, sms = PackedDims(), load_library(), _int32(sms, "sms")
+    _check(lib.vsa_packed_query(ctypes.byref(desc), sms, ctypes.byref(d), None, None), "vsa_packed_query")
     items, first = np.zeros((max(1, d.items), 4), np.int32), np.zeros(d.ctas + 1, np.int32)
-    _check(lib.vsa_packed_query(ctypes.byref(desc), int(sms), ctypes.byref(d), items.ctypes.data, first.ctypes.data),
+    _check(lib.vsa_packed_query(ctypes.byref(desc), sms, ctypes.byref(d), items.ctypes.data, first.ctypes.data),
            "vsa_packed_query")
     return dict(d.as_dict(), items=items[:d.items], first=first)
 

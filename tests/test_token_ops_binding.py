@@ -99,3 +99,29 @@ def test_a_collected_plan_is_freed_by_the_next_call_that_may(vsa, monkeypatch):
     gc.collect()
     vsa.vsa_packed_plan((9,), 1).destroy()
     assert lib.calls[8:] == [("plan", 104), ("destroy", 104)]
+
+
+WRAPS = 1 << 32  # a multiple of 2^32 added to a 32-bit field would vanish
+
+
+@pytest.mark.parametrize("kw", [dict(lengths=(5 - WRAPS,)), dict(lengths=(5 + WRAPS,)), dict(heads=4 + WRAPS, kv_heads=4),
+                                dict(kv_heads=1 + WRAPS), dict(head_dim=64 + WRAPS), dict(sms=148 + WRAPS)])
+def test_packed_numbers_past_32_bits(vsa, kw):
+    with pytest.raises(ValueError):
+        vsa.vsa_packed_query(**dict(dict(lengths=(5, 7), heads=4, kv_heads=2, head_dim=64), **kw))
+
+
+@pytest.mark.parametrize("kw", [dict(head_dim=64 + WRAPS, sections=(8,)), dict(head_dim=64, sections=(8 + WRAPS,)),
+                                dict(head_dim=64, sections=(8 - WRAPS,)),
+                                dict(head_dim=64, inv_freq=[1.0] * 32, axis=[0] * 31 + [WRAPS]),
+                                dict(head_dim=64, inv_freq=[1.0] * 32, axis=[0] * 32, n_axes=1 + WRAPS)])
+def test_rope_numbers_past_32_bits(vsa, kw):
+    with pytest.raises(ValueError):
+        vsa.vsa_rope_create(**kw)
+
+
+def test_norm_width_past_32_bits(no_device):
+    """A row of 2^32 + 8 elements is not a row of 8."""
+    wide = torch.empty(1, WRAPS + 8, dtype=torch.bfloat16, device="meta")
+    with pytest.raises(ValueError):
+        no_device.vsa_rms_norm(wide, out=wide)
