@@ -10,6 +10,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <memory>
 #include <mutex>
 #include <new>
 #include <queue>
@@ -1695,7 +1696,6 @@ vsa_status vsa_packed_query(const vsa_packed_desc* d, int32_t sms, vsa_packed_di
 }
 
 vsa_status vsa_packed_plan(const vsa_packed_desc* d, void* stream, vsa_packed_plan_t* out) {
-  vsa_packed_plan_s* p = nullptr;
   try {
     if (out == nullptr) return fail(VSA_ERR_INVALID_ARG, "out is NULL");
     *out = nullptr;
@@ -1709,25 +1709,23 @@ vsa_status vsa_packed_plan(const vsa_packed_desc* d, void* stream, vsa_packed_pl
     if (major != 10 || minor != 0)
       return fail(VSA_ERR_DEVICE, "libvsa is built for sm_100a; device " + std::to_string(dev) + " is sm_" +
                                       std::to_string(major) + std::to_string(minor));
-    p = new vsa_packed_plan_s();
+    struct Release {
+      void operator()(vsa_packed_plan_s* q) const {
+        cudaFree(q->d_table);
+        delete q;
+      }
+    };
+    std::unique_ptr<vsa_packed_plan_s, Release> p(new vsa_packed_plan_s());  // until it is the caller's
     p->device = dev;
     p->heads = d->heads;
     p->kv_heads = d->kv_heads;
     p->D = d->head_dim;
     p->causal = d->causal;
-    vsa_status st = packed_schedule(d, sms, &p->dims, &p->items, &p->first);
-    if (st != VSA_OK) {
-      delete p;
-      return st;
-    }
-    st = with_head_dim(p->D, [&](auto dc) -> vsa_status {
+    VSA_TRY(packed_schedule(d, sms, &p->dims, &p->items, &p->first));
+    VSA_TRY(with_head_dim(p->D, [&](auto dc) -> vsa_status {
       constexpr int D = decltype(dc)::value;
       return allow_smem(vsa::packed_attn_kernel<D>, vsa::PackedLayout<D>::bytes());
-    });
-    if (st != VSA_OK) {
-      delete p;
-      return st;
-    }
+    }));
     const size_t item_bytes = align256(p->items.size() * sizeof(vsa::PackedItem));
     const size_t first_bytes = align256(p->first.size() * sizeof(int32_t));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1746,15 +1744,10 @@ vsa_status vsa_packed_plan(const vsa_packed_desc* d, void* stream, vsa_packed_pl
       // calls may come on other streams than this one: the table is there when the plan is
       if (e == cudaSuccess) e = cudaStreamSynchronize(s);
     }
-    if (e != cudaSuccess) {
-      cudaFree(p->d_table);
-      delete p;
-      return fail(VSA_ERR_CUDA, std::string("packed plan upload: ") + cudaGetErrorString(e));
-    }
-    *out = p;
+    if (e != cudaSuccess) return fail(VSA_ERR_CUDA, std::string("packed plan upload: ") + cudaGetErrorString(e));
+    *out = p.release();
     return VSA_OK;
   } catch (const std::exception&) {
-    delete p;
     return vsa::set_error(VSA_ERR_INVALID_ARG, "out of host memory");
   }
 }
