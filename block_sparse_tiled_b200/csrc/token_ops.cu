@@ -20,8 +20,6 @@ namespace {
 
 using vsa::set_error;
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 __device__ __forceinline__ void unpack8(const uint4& u, float* f) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -561,9 +559,10 @@ vsa_status check_stride(const char* what, int64_t rows, int64_t ld, int64_t widt
     if (s_ != VSA_OK) return s_;      \
   } while (0)
 
-vsa_status check_ptr(const char* what, const void* p) {
+vsa_status check_ptr(const char* what, const void* p, unsigned align = 16) {
   if (p == nullptr) return set_error(VSA_ERR_INVALID_ARG, "%s is NULL", what);
-  if (!aligned16(p)) return set_error(VSA_ERR_INVALID_ARG, "%s must be 16-byte aligned", what);
+  if ((reinterpret_cast<uintptr_t>(p) & (align - 1)) != 0)
+    return set_error(VSA_ERR_INVALID_ARG, "%s must be %u-byte aligned", what, align);
   return VSA_OK;
 }
 
@@ -609,7 +608,7 @@ vsa_status vsa_rms_norm(const vsa_rms_norm_args* p, void* stream) {
   VSA_TRY(check_stride("x", p->rows, p->x_stride, p->width, false));
   VSA_TRY(check_stride("out", p->rows, p->out_stride, p->width, true));
   if (p->weight != nullptr) VSA_TRY(check_ptr("weight", p->weight));
-  if (p->out_e4m3) VSA_TRY(check_ptr("scale", p->scale));
+  if (p->out_e4m3) VSA_TRY(check_ptr("scale", p->scale, 4));
   if (res) {
     VSA_TRY(check_ptr("residual", p->residual));
     VSA_TRY(check_stride("residual", p->rows, p->residual_stride, p->width, false));
@@ -758,7 +757,7 @@ vsa_status vsa_qk_rope(vsa_rope r, const vsa_qk_rope_args* p, void* stream) {
   if (p->pos_rows < 1 || p->tokens % p->pos_rows != 0)
     return set_error(VSA_ERR_SHAPE, "pos_rows must divide the %lld tokens, got %lld", static_cast<long long>(p->tokens),
                      static_cast<long long>(p->pos_rows));
-  VSA_TRY(check_ptr("positions", p->positions));
+  VSA_TRY(check_ptr("positions", p->positions, 4));
   const auto rows_of = [&](const char* name, const void* base, int heads, int64_t ld, int64_t hd) {
     return Operand{name, {base, p->tokens, ld * 2, heads, hd * 2, D * 2}};
   };

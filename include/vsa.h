@@ -22,7 +22,7 @@
  *    allocates device memory per call; a plan allocates its own small tables
  *    once, in vsa_plan_tiles, and frees them in vsa_plan_destroy.
  *  - bf16 tensors are raw IEEE bfloat16 bit patterns (vsa_bf16).  Every
- *    device pointer must be 16-byte aligned.
+ *    device pointer must be 16-byte aligned, where nothing else is said.
  *  - `stream` is a cudaStream_t passed as void*; NULL is the legacy default
  *    stream.  All device work is asynchronous on it; no entry point but
  *    vsa_device_status synchronises.
@@ -440,7 +440,7 @@ typedef struct vsa_rms_norm_args {
   const void* weight;   /* [width]; NULL: ones */
   void* out;
   void* residual_out;
-  float* scale; /* [rows] with out_e4m3 */
+  float* scale; /* [rows] with out_e4m3; 4-byte aligned */
   int64_t x_stride, residual_stride, out_stride, residual_out_stride;
 } vsa_rms_norm_args;
 vsa_status vsa_rms_norm(const vsa_rms_norm_args* args, void* stream);
@@ -479,7 +479,7 @@ vsa_status vsa_rope_destroy(vsa_rope r);
  * y = x * (1 / sqrt(mean(x^2) + eps)) * weight over the head row (y = x without),
  * then each pair (a, b) turns by angle = position * f_p:
  *   (a cos - b sin, a sin + b cos).
- * positions: [pos_rows, n_axes], int32 or binary32; token t uses row
+ * positions: [pos_rows, n_axes], int32 or binary32, 4-byte aligned; token t uses row
  * t % pos_rows (pos_rows = L serves a [B, L, ..] batch).  The angle is the
  * binary64 product reduced in binary64, so far positions keep their accuracy.
  *  - strides: elements between tokens and between heads, multiples of 8, so q

@@ -82,3 +82,20 @@ def test_norm_output_beside_and_over_the_inputs(vsa):
     want = vsa.vsa_rms_norm(x, residual=r)
     vsa.vsa_rms_norm(x, residual=r, out=buf[:rows, 2 * C:], residual_out=x)  # the stream moves from r to x
     assert torch.equal(buf[:rows, 2 * C:], want[0]) and torch.equal(x, want[2])
+
+
+def test_chunks_of_positions_and_scales(vsa):
+    """A chunk of the positions, and of a buffer of scales, from any row on."""
+    T, D = 61, 64
+    rope = vsa.vsa_rope_create(D, (10, 12, 10))
+    pos = torch.randint(0, 99, (T, 3), dtype=torch.int32, device="cuda")
+    q, x = randn(3, T, 2, D), randn(4, T, 128)
+    every, _ = vsa.vsa_qk_rope(rope, q, None, pos)
+    codes, scales, _ = vsa.vsa_rms_norm(x, out_dtype=torch.float8_e4m3fn)
+    chunked = torch.full((T + 3,), 7.0, device="cuda")
+    for a, b in ((0, 5), (5, 6), (6, 61)):
+        part, _ = vsa.vsa_qk_rope(rope, q[a:b], None, pos[a:b])
+        assert torch.equal(part, every[a:b])
+        out, _, _ = vsa.vsa_rms_norm(x[a:b], out_dtype=torch.float8_e4m3fn, scale=chunked[1 + a:1 + b])
+        assert torch.equal(out.view(torch.uint8), codes[a:b].view(torch.uint8))
+    assert torch.equal(chunked[1:T + 1], scales) and (chunked[[0, T + 1, T + 2]] == 7).all()

@@ -160,3 +160,15 @@ QKV = dict(q=2 * A, k=2 * A + 256, q_stride=256, k_stride=256)  # [4, 2 + 1 + 1,
 def test_rope_layouts_that_stay(vsa, over):
     r = vsa.vsa_rope_create(64, (32,))
     assert launched(vsa, "vsa_qk_rope", r.handle, ctypes.byref(vsa.QkRopeArgs(**dict(ROPE, **over))))
+
+
+def test_positions_and_scales_may_start_anywhere(vsa):
+    """Both are read and written a number at a time: a chunk of a longer table starts at any row of it."""
+    r = vsa.vsa_rope_create(64, (32,))
+    assert launched(vsa, "vsa_qk_rope", r.handle, ctypes.byref(vsa.QkRopeArgs(**dict(ROPE, positions=A + 12))))
+    assert launched(vsa, "vsa_rms_norm", ctypes.byref(vsa.RmsNormArgs(**dict(NORM, out_e4m3=1, scale=4 * A + 20))))
+    for size in (1, 2):
+        a = vsa.QkRopeArgs(**dict(ROPE, positions=A + size))
+        assert status(vsa, "vsa_qk_rope", r.handle, ctypes.byref(a)) == "VSA_ERR_INVALID_ARG"
+        n = vsa.RmsNormArgs(**dict(NORM, out_e4m3=1, scale=4 * A + size))
+        assert status(vsa, "vsa_rms_norm", ctypes.byref(n)) == "VSA_ERR_INVALID_ARG"
