@@ -31,11 +31,17 @@
 // between a sequence's end and the next multiple of 16 with zeros before the product may read them.
 //
 // What bounds it: the softmax chain of a block, about 1,500 cycles where its two products take 1,024 at D = 128
-// (tensor and special function pipes both 63% busy), then the power limit on long prompts.  40 heads on 8, D = 128,
-// causal, one sequence of 8192: 620 to 665 us, 1,030 to 1,107 TFLOP/s; 56 heads, D = 96, four sequences of 700 to 2048,
-// not causal: 207 to 215 us, 840 to 870 TFLOP/s; 64 heads on 8, D = 64, ragged, causal: 379 us, 652 TFLOP/s (9.7e8
-// exponentials take 214).  Short items are a chain of load, product, softmax, product and store of about 3,600
-// cycles: 24 prompts of 1 to 1000 tokens 71.5 us.
+// (tensor and special function pipes both 63% busy), then the power limit on long prompts.  One thread loads 128 scores,
+// takes their maximum and waits for the other group's before its first exponential.  Calls in a row, with the sampled SM
+// clock (in brackets: bursts of nine calls, before the power limit lowers it):
+//   40 heads on 8, D = 128, causal, one sequence of 8192                 675 us at 1,515 MHz, 1,018 TFLOP/s (575 to 590)
+//   56 heads, D = 96, four sequences of 700 to 2048, not causal          244 us at 1,582 MHz, 739 TFLOP/s (206 to 211)
+//   64 heads on 8, D = 64, ragged, causal (9.7e8 exponentials: 214 us)   390 us at 1,950 MHz, 634 TFLOP/s (381)
+//   40 heads on 8, D = 128, causal, 24 prompts of 1 to 1000 tokens       78 us at 1,770 MHz (69.6)
+// An item's first block is a chain of load, product, softmax, product and store that little overlaps (one O buffer; each
+// thread stores its own row): the time from 4 to 8 one-block items a CTA grows by 8,600 cycles an item of 128 tokens at
+// D = 128, 6,300 at D = 96, 4,600 at D = 64; 6,000 for 25 tokens of five heads, 3,400 for single tokens.  A call on one token
+// takes 5.2 us: the launch, the set-up (TMEM, barriers, tensor maps) and that item.
 //
 // Roles (352 threads): warps 0..3 and 4..7 softmax of even and odd blocks, and the epilogue (half of O's columns
 // each); 8 TMA loads; 9 issues S and owns TMEM, 10 issues P.V.  Every mbarrier wait is bounded.
@@ -115,8 +121,8 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
 }
 
 // mbar_wait and mbar_wait_drain without a call (the softmax's registers would be saved around it): the abort flag at the
-// first look that fails and at every eighth, the time at every 1024th.  With kIdle, for the warps that run ahead, kIdleNs
-// of sleep between looks.
+// first look that fails and at every eighth, the time at every 1024th.  With kIdle, for the loader and the two issuers, kIdleNs
+// of sleep between looks (their waits lie on the chain of an item's first block too).
 constexpr unsigned kIdleNs = 100;
 template <bool kIdle = false>
 __device__ __forceinline__ bool packed_wait(uint64_t* bar, uint32_t parity, const WaitCtl& ctl, int site,

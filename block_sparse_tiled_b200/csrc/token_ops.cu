@@ -1,6 +1,7 @@
 // Row operators of a block around the attention, in sequence order: the root-mean-square norm with the
 // residual's addition (vsa_rms_norm), and the head norm and rotary positions of Q and K (vsa_qk_rope).
-// Both are bound by HBM traffic: each reads its inputs once and writes its outputs once.
+// Each reads its inputs once and writes its outputs once.  HBM bounds the norm and the rotary positions of long wide
+// sequences; instruction issue bounds the rotary positions at D = 96.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -67,19 +68,6 @@ __device__ __forceinline__ uint4 pack8(const float* f) {
   return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
 }
 
-// Eight values of a bf16 or binary32 row, starting at element 8 * chunk (16-byte aligned).
-template <bool kF32>
-__device__ __forceinline__ void load8(const void* row, int chunk, float* f) {
-  if constexpr (kF32) {
-    const float4* p = reinterpret_cast<const float4*>(row) + 2 * chunk;
-    const float4 a = p[0], b = p[1];
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-  } else {
-    unpack8(reinterpret_cast<const uint4*>(row)[chunk], f);
-  }
-}
-
 // ---------------------------------------------------------------------------------------------
 // vsa_rms_norm.  With t = x + r (binary32):
 //   r' = t rounded to the residual's type,   y = t * rsqrt(mean(t^2) + eps) * w,
@@ -109,11 +97,12 @@ struct NormArgs {
 
 enum : int { kNoRes = 0, kResBf16 = 1, kResF32 = 2 };
 
-// Threads of a row at most, by its chunks per thread, and the CTAs per SM to compile for.
 // Threads of a row at most, by its chunks per thread, and the CTAs per SM to compile for (more of them hold more loads
 // in flight, until the registers for them run out: 14,208 rows of 5376 without a residual at 3 chunks 58 us at two
 // CTAs, 51 at three, 55 at four; 30,000 bf16-residual rows of 4096 at 2 chunks 155 us at four, 137 at three; 75,008 rows
-// of 5376 with a residual at 3 chunks 433 us at two, 509 at three).
+// of 5376 with a residual at 3 chunks 433 us at two, 509 at three).  Four chunks, the widths above 6144, take one CTA of up
+// to 512 threads; a binary32 residual then spills 16 to 32 bytes.  At 1.6e8 elements and widths of 6152 to 16384: without
+// a residual 5.4 to 6.2 TB/s (8-bit 4.2 to 5.2), bf16 residual 5.8 to 6.6, binary32 residual 5.5 to 6.3.
 template <int kC>
 constexpr int kNormThreads = kC == 4 ? 512 : 256;
 template <int kC, bool kRes>
@@ -521,8 +510,8 @@ vsa_status launch(const char* what, K kernel, unsigned grid, unsigned block, siz
   return VSA_OK;
 }
 
-// As many CTAs as the GPU holds at once: a second wave of them would read its weights again and end unevenly
-// (a 4096-wide binary32 residual: 204 -> 270 us at half the CTAs, 272 at 3.5 of 4).
+// As many CTAs as the GPU holds at once.  75,008 rows of 5376, bf16 residual, 8-bit: 432 us; at half of them 572, at 7/8
+// 458, at 1.5 times 506, at twice 434 (14,208 rows without a residual: 51; 65, 53, 55, 52).
 template <int kRes, bool kF8, bool kWF32, bool kWarp>
 vsa_status launch_norm(const NormArgs& a, int per, int threads, int64_t groups, int sms, void* stream) {
   static std::atomic<int> held[4][33];  // CTAs per SM, by chunks per thread and warps; 0: not asked yet
@@ -654,8 +643,9 @@ vsa_status vsa_rms_norm(const vsa_rms_norm_args* p, void* stream) {
   if (e != cudaSuccess) return set_error(VSA_ERR_CUDA, "rms_norm: %s", cudaGetErrorString(e));
   // Chunks per thread and threads per row: a warp up to 1024 elements; beyond, two to four chunks, for about 256 threads
   // (5376 elements without a residual: 51 us at 3 chunks, 58 at 2, 96 at one; 40,000 rows of 2048: 52.5 us at two
-  // chunks, 61.6 at one).  A binary32 residual of 385 to 512 chunks takes three (30,000 rows of 4096: 245 us, 260 at two;
-  // with 8-bit output 213, 243 at two).
+  // chunks, 61.6 at one).  A binary32 residual of 385 to 512 chunks takes three: 30,000 rows of 3080, 3584 and 4096 in
+  // 196, 237 and 244 us, at two 201, 232 and 261 (8-bit output 174, 213 and 212; 177, 209 and 242).  Without one, and with
+  // a bf16 residual and 8-bit output, two are as good or better at 4096 (77 us, 78 at three; 136, 147).
   const int chunks = p->width / 8;
   const bool warp = chunks <= 128;
   const int wide = res && p->residual_f32 && chunks <= 512 ? 192 : 256;

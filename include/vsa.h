@@ -20,12 +20,15 @@
  *    tensor and every workspace and must keep them alive until the work on
  *    `stream` has finished.  The library never frees caller memory and never
  *    allocates device memory per call; a plan allocates its own small tables
- *    once, in vsa_plan_tiles, and frees them in vsa_plan_destroy.
+ *    once, in vsa_plan_tiles or vsa_packed_plan, and frees them in
+ *    vsa_plan_destroy or vsa_packed_destroy.
  *  - bf16 tensors are raw IEEE bfloat16 bit patterns (vsa_bf16).  Every
  *    device pointer must be 16-byte aligned, where nothing else is said.
  *  - `stream` is a cudaStream_t passed as void*; NULL is the legacy default
- *    stream.  All device work is asynchronous on it; no entry point but
- *    vsa_device_status synchronises.
+ *    stream.  All device work is asynchronous on it.  These entry points wait
+ *    for `stream`: vsa_packed_plan, vsa_device_status, vsa_packed_status and the
+ *    self-tests.  vsa_plan_destroy and vsa_packed_destroy wait for the device.
+ *    No other one synchronises.
  *  - Layouts (row-major, last index fastest):
  *      sequence order : q, k, v, out  [B, L, H, D];  gate [B, L, H], or [B, L, H*D]
  *                       with vsa_geometry.gate_per_channel
@@ -42,9 +45,10 @@
  *    a multiple of 4.  Video tokens follow the prefix in raster (t, h, w)
  *    order, w fastest.  Inside a tile the valid tokens come first, in
  *    sequence (prefix) or raster (cube) order, then zero pads.
- *  - A plan's device status word and the attention kernels' work counters are
+ *  - A vsa_plan's device status word and the attention kernels' work counters are
  *    shared by every call made with that plan: calls with one plan must not
- *    overlap on the GPU (use one plan per concurrent stream).
+ *    overlap on the GPU (use one plan per concurrent stream).  Calls with one
+ *    packed plan may.
  *  - The attention may run as two kernels: row blocks that share their key
  *    list (the dense prefix query tiles, when B * H * ceil(P/2) reaches the
  *    SM count; every query tile with 128-token tiles) go two at a time to a
@@ -54,7 +58,8 @@
  *  - Errors: argument and shape errors are detected on the host and returned
  *    synchronously with nothing launched; a failed launch returns
  *    VSA_ERR_CUDA; device-side failures (a bounded wait that ran out) are
- *    recorded in the plan's device status word, read with vsa_device_status.
+ *    recorded in the plan's device status word, read with vsa_device_status
+ *    (a packed plan's with vsa_packed_status).
  *    vsa_last_error() returns a message for the calling thread's last error.
  *    There is no fallback path: an unsupported case is an error.
  */
