@@ -978,9 +978,9 @@ class PackedPlan:
             load_library().vsa_packed_destroy(self._h)
             self._h = None
 
-    def __del__(self):
+    def __del__(self, collected=_collected_plans):  # (the module's names may be gone at the interpreter's end)
         if getattr(self, "_h", None) is not None:
-            _collected_plans.append(self._h)
+            collected.append(self._h)
 
 
 def vsa_packed_plan(lengths, heads, kv_heads=None, head_dim=128, causal=True, softmax_scale=0.0, stream=None) -> PackedPlan:

@@ -125,3 +125,19 @@ def test_norm_width_past_32_bits(no_device):
     wide = torch.empty(1, WRAPS + 8, dtype=torch.bfloat16, device="meta")
     with pytest.raises(ValueError):
         no_device.vsa_rms_norm(wide, out=wide)
+
+
+def test_a_plan_alive_at_exit_says_nothing():
+    """At the interpreter's end a module's names may be gone before its plans."""
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = ("import sys; sys.path[:0] = [%r, %r]\n"
+            "import block_sparse_tiled_b200 as vsa, test_token_ops_binding as t\n"
+            "lib = t.FakeLibrary(vsa); vsa.load_library = lambda *_: lib; vsa._stream = lambda *_: None\n"
+            "plan = vsa.vsa_packed_plan((5,), 1)\n"
+            "calls = {'attn': lambda: plan}\n" % (root, os.path.join(root, "tests")))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True)
+    assert r.returncode == 0 and r.stderr == ""
