@@ -707,7 +707,9 @@ def vsa_rms_norm(x, weight=None, eps=1e-6, residual=None, out=None, residual_out
     shape = x.shape
     if not shape or shape[-1] == 0:
         raise ValueError(f"x must end in a dimension that is not empty, got {tuple(shape)}")
-    C = _int32(shape[-1], "the width")
+    C = shape[-1]
+    if C > 0x7fffffff:
+        raise ValueError(f"the width must fit 32 bits, got {C}")
     rows = x.numel() // C
     if out is None:
         out = _empty(shape, out_dtype or _BF16, x.device, stream)
@@ -864,7 +866,7 @@ def vsa_qk_rope(rope, q, k, positions, q_weight=None, k_weight=None, eps=1e-6, q
         raise ValueError(f"positions must be a contiguous [tokens, {axes}], got {tuple(positions.shape)}")
     rows = positions.numel() // axes
     # the library repeats any number of rows that divides the tokens (and refuses others); here only a batch's sequences do
-    if rows != tokens and not (q.dim() == 4 and rows == q.shape[1]) and rows > 0 and tokens % rows == 0:
+    if rows != tokens and rows > 0 and tokens % rows == 0 and not (q.dim() == 4 and rows == q.shape[1]):
         fits = f"{tokens}" if q.dim() == 3 else f"{q.shape[1]} or {tokens}"
         raise ValueError(f"positions must have {fits} rows for q {tuple(q.shape)}, got {rows}")
     if q_out is None:
