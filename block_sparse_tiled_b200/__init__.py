@@ -230,7 +230,9 @@ def _allocating_on(stream, device):
     if stream is None:
         return contextlib.nullcontext()
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
+        handle = int(stream)
+        # torch knows the legacy default stream as 0 only, not by its other name, cudaStreamLegacy = 1
+        stream = torch.cuda.ExternalStream(0 if handle == 1 else handle, device=device)
     return torch.cuda.stream(stream)
 
 

@@ -91,3 +91,19 @@ def test_forward_allocates_on_the_calls_stream(vsa, monkeypatch):
     vsa.vsa_forward_parts(plan, [q], [k], [v], [gate], [out], 0, stream=s)
     s.synchronize()
     assert at == [s, s] and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("raw", [0, 1, 2])
+def test_raw_handles_of_the_default_streams(vsa, raw):
+    """0 and 1 name the legacy default stream, 2 the calling thread's own."""
+    x, w = randn(20, 30, 512), randn(21, 512)
+    q, k, v = randn(22, 40, 4, 64), randn(23, 40, 2, 64), randn(24, 40, 2, 64)
+    plan = vsa.vsa_packed_plan((30,), 4, 2, 64)
+    want = vsa.vsa_rms_norm(x, w, residual=x, out_dtype=E4M3)
+    attn = vsa.vsa_packed_attn(plan, q, k, v)
+    torch.cuda.synchronize()
+    got = vsa.vsa_rms_norm(x, w, residual=x, out_dtype=E4M3, stream=raw)
+    out = vsa.vsa_packed_attn(plan, q, k, v, stream=raw)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0].view(torch.uint8), want[0].view(torch.uint8)) and torch.equal(got[1], want[1])
+    assert torch.equal(got[2], want[2]) and torch.equal(out, attn)
